@@ -392,6 +392,150 @@ int ssm_dtproj_bwd(const ssm_dtshape* shape, const void* u, const void* w, const
                    void* du, float* dw, float* dbias, void* ws, size_t ws_bytes,
                    ssm_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Short causal convolution in front of the scan.  One filter of W = 2..4 taps per channel, over
+ * the last W steps, with an optional bias and SiLU; per batch b and channel d:
+ *     v_t = bias[d] + sum_{j<W} w[d,j] x_{t-(W-1)+j}       (x_{-1}, x_{-2}, ..: the state s0, or zero)
+ *     y_t = v_t sigmoid(v_t)  with SSM_CONV_SILU,  y_t = v_t without
+ * The state of a sequence is its last W-1 inputs, oldest first: s0 is the state before step 0 and
+ * sL the state after step L-1 (with L < W-1 it still holds the newest entries of s0); passing sL of
+ * one call as s0 of the next continues a sequence.
+ *
+ * 8-bit checkpoint.  The forward can also write its input in 8 bits, from which
+ * ssm_conv_restore recomputes y (the scan's input) and ssm_conv_bwd takes its gradient, so that
+ * neither x nor y has to be kept for the backward: 33/32 bytes an element.  In every row the 32
+ * channels 32k..32k+31 (fewer at the end of the row) share one power of two: q[b,t,d] is an int8,
+ * qe[b,t,k] a byte, and the value is q 2^(qe - 127).  With a the group's largest magnitude, the step
+ * is 2^(floor(log2 a) - 6), or twice that where a would round past 127, never below 2^-126; q is x
+ * over the step rounded to nearest, ties to even, so a value is off by at most half a step (from
+ * a = 2^127 on, where a larger step could not be restored, by less than one: 127 is the limit).  A
+ * group of zeros has qe = 0.  A group that holds an infinity or a NaN has qe = 255 and q = 0: all
+ * its values restore as NaN.  The gradient is the one at the restored x.
+ *
+ * Layout: x, y, dy, dx [B, L, D] in the io type, each with its own row stride (elements from one
+ * step to the next; batch b starts L strides after batch b-1), so that one half of a projection's
+ * [B, L, 2D] rows can be used in place; s0, sL, dsL, ds0 [B, W-1, D] dense, io type; w, dw [D, W] and
+ * bias, dbias [D] fp32; q [B, L, D] int8 and qe [B, L, ceil(D/32)] bytes, dense.  Sums are
+ * fp32; y, dx and ds0 are rounded to the io type once.  Outputs must not overlap inputs.
+ */
+typedef struct ssm_conv_shape {
+    int64_t batch;   /* B >= 0, at most 65535 */
+    int64_t seqlen;  /* L >= 0, at most 2^30 */
+    int64_t dim;     /* D >= 1, at most 2^22; D * sizeof(io) a multiple of 16 bytes */
+    int64_t ldx;     /* row strides of x, y, dy, dx in elements: 0 = D, else at least D and a */
+    int64_t ldy;     /*   multiple of 16 bytes; only those of the call's own arrays are used,  */
+    int64_t lddy;    /*   all are checked                                                      */
+    int64_t lddx;
+    int32_t width;   /* W, one of 2, 3, 4 */
+    int32_t io;      /* ssm_dtype */
+    int32_t flags;   /* SSM_CONV_SILU or 0 */
+    int32_t reserved; /* must be 0 */
+} ssm_conv_shape;
+
+#define SSM_CONV_SILU 1 /* flags of ssm_conv_shape and ssm_conv_serve */
+
+/* Forward.  bias, s0 (zero), sL (not written) and the pair q, qe (not written) may be NULL.
+ * Enqueues 1 kernel; needs no workspace.  Returns an ssm_status. */
+int ssm_conv_fwd(const ssm_conv_shape* shape, const void* x, const float* w, const float* bias,
+                 const void* s0, void* y, void* sL, int8_t* q, uint8_t* qe, ssm_stream_t stream);
+
+/* y from the 8-bit checkpoint (what the forward gives for the restored x).  ldx is not used.
+ * bias and s0 as for the forward.  Enqueues 1 kernel; needs no workspace. */
+int ssm_conv_restore(const ssm_conv_shape* shape, const int8_t* q, const uint8_t* qe,
+                     const float* w, const float* bias, const void* s0, void* y,
+                     ssm_stream_t stream);
+
+/* Workspace bytes of ssm_conv_bwd (status word, partial sums of dw and dbias); 0 for an invalid
+ * shape. */
+size_t ssm_conv_workspace_bytes(const ssm_conv_shape* shape);
+
+/* Gradient of sum(dy y) + sum(dsL sL) for the forward above, from x or from q, qe (give x, or both
+ * of q and qe with x NULL).  With v and g_t = dy_t dy_t/dv_t (zero past the end):
+ *     dx_t = sum_{k<W} w[d,W-1-k] g_{t+k} (+ dsL where sL holds x_t),  ds0 likewise,
+ *     dw[d,j] = sum_{b,t} g_t x_{t-(W-1)+j},   dbias[d] = sum_{b,t} g_t.
+ * bias, s0, dsL (zero), dbias and ds0 (not written) may be NULL.  Enqueues 2 kernels (none when B or
+ * L is 0).  ws: at least ssm_conv_workspace_bytes(shape).  Returns an ssm_status. */
+int ssm_conv_bwd(const ssm_conv_shape* shape, const void* x, const int8_t* q, const uint8_t* qe,
+                 const float* w, const float* bias, const void* s0, const void* dy,
+                 const void* dsL, void* dx, float* dw, float* dbias, void* ds0,
+                 void* ws, size_t ws_bytes, ssm_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Serving: the convolution and the scan over packed prompts and over single tokens, with the
+ * states of all live sequences in pools that the caller owns,
+ *     convolution pool [slots, W-1, D] io type (oldest input first),  scan pool [slots, D, N] fp32
+ * (one entry as s0 / sL and h0 / hL of the calls above).
+ *
+ * Prompts.  The rows of all sequences lie one after another: sequence s owns rows offsets[s] ..
+ * offsets[s+1]-1 (offsets: S+1 int32 on the device, not decreasing, within 0..rows; a sequence may be
+ * empty) and pool entry slot[s] (int32 on the device).  carry[s] != 0: it continues from that entry;
+ * carry[s] == 0, or carry NULL: it starts from zero.  The state after its last row is written back
+ * to the entry.  A slot of -1 (any negative number): no entry; the sequence starts from zero and
+ * its state is dropped.  Rows outside every sequence are neither read nor written.
+ *
+ * Single tokens.  Row b is the next token of the sequence in pool entry slot[b]; slot NULL: entry
+ * b.  A negative slot marks a padding row: nothing of it is read or written, y included.
+ *
+ * What the device finds in offsets and slot is checked there: a sequence or row whose offsets or
+ * slot are out of range, one longer than max_len, and each that names an entry which an earlier one of
+ * the same call names too is left out (its rows of y and its entry stay as they are), and
+ * SSM_ERR_INVALID_ARG is recorded in the status word.  SSM_ERR_NONFINITE is recorded as for the
+ * other scans.  ws may be NULL (ws_bytes 0) where a call needs only the status word (256 bytes): then
+ * nothing is recorded, and the call is one kernel with no memset before it.
+ *
+ * Row strides in elements, 0 = dense; at least the row's length; of x, y, delta_raw and z a multiple
+ * of 16 bytes with 16-byte aligned pointers, of Bm and Cm a multiple of 4 elements with pointers aligned
+ * to 4 elements: columns of a projection's output are used in place.  offsets and slot are
+ * aligned to 4 bytes.  Outputs must not overlap inputs.
+ */
+typedef struct ssm_conv_serve {
+    int64_t rows;   /* rows of x and y, 0..2^30 (single tokens: the batch, at most 65535) */
+    int64_t seqs;   /* S, 0..65535 (single tokens: must be 0) */
+    int64_t dim;    /* D as above */
+    int64_t slots;  /* entries of the pool, 0..2^30 */
+    int64_t ldx, ldy;
+    int32_t width;  /* W, one of 2, 3, 4 */
+    int32_t io;     /* ssm_dtype */
+    int32_t flags;  /* SSM_CONV_SILU or 0 */
+    int32_t reserved; /* must be 0 */
+} ssm_conv_serve;
+
+int ssm_conv_prompt(const ssm_conv_serve* shape, const void* x, const float* w, const float* bias,
+                    const int32_t* offsets, const int32_t* slot, const uint8_t* carry, void* pool,
+                    void* y, void* ws, size_t ws_bytes, ssm_stream_t stream);
+
+int ssm_conv_step(const ssm_conv_serve* shape, const void* x, const float* w, const float* bias,
+                  const int32_t* slot, void* pool, void* y, void* ws, size_t ws_bytes,
+                  ssm_stream_t stream);
+
+/* Scan, as ssm_scan_fwd_ex from the entry's state, without checkpoints; with z the output is gated,
+ *     y_t = (sum_n Cm_t,n h_t,n + Dskip[d] x_t) z_t sigmoid(z_t)        (z NULL: not gated).
+ * x, delta_raw, z, y [rows, D], Bm, Cm [rows, N] io type; A_log [D, N], Dskip [D] fp32. */
+typedef struct ssm_scan_serve {
+    int64_t rows, seqs, dim, dstate, slots; /* dim at most 2^20, N one of 4, 8, 16; else as above */
+    int64_t max_len; /* prompts: no sequence is longer; 0 = rows.  The time split is planned by it.
+                        Single tokens: must be 0 */
+    int64_t ldx, lddelta, ldz, ldb, ldc, ldy;
+    int32_t io;             /* ssm_dtype */
+    int32_t discretization; /* ssm_discretization */
+} ssm_scan_serve;
+
+/* Workspace bytes of ssm_scan_prompt (at least 256); 0 for an invalid shape. */
+size_t ssm_scan_prompt_workspace_bytes(const ssm_scan_serve* shape);
+
+/* Prompts.  Enqueues 1 kernel, or 3 when max_len is above the time segment that fills the GPU. */
+int ssm_scan_prompt(const ssm_scan_serve* shape, const void* x, const void* delta_raw,
+                    const float* A_log, const void* Bm, const void* Cm, const float* Dskip,
+                    const void* z, const int32_t* offsets, const int32_t* slot,
+                    const uint8_t* carry, float* pool, void* y, void* ws, size_t ws_bytes,
+                    ssm_stream_t stream);
+
+/* Single tokens.  Enqueues 1 kernel. */
+int ssm_scan_step(const ssm_scan_serve* shape, const void* x, const void* delta_raw,
+                  const float* A_log, const void* Bm, const void* Cm, const float* Dskip,
+                  const void* z, const int32_t* slot, float* pool, void* y, void* ws,
+                  size_t ws_bytes, ssm_stream_t stream);
+
 /* Number of kernels one ssm_scan_fwd (backward == 0) / ssm_scan_bwd (backward == 1) call
  * enqueues for this shape (0 for an empty problem, -1 for an invalid shape); backward == 2 counts
  * a backward with SSM_FUSED_SUMS on a device that holds 444 of its CTAs at once (592 for N = 16),

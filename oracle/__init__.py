@@ -59,6 +59,10 @@ def _load():
             lib.ssm_oracle_dtproj.restype = ctypes.c_int
             lib.ssm_oracle_dtproj_bwd.argtypes = [I64, I64, I64] + [P] * 6
             lib.ssm_oracle_dtproj_bwd.restype = ctypes.c_int
+            lib.ssm_oracle_conv.argtypes = [I64] * 4 + [ctypes.c_int] + [P] * 12
+            lib.ssm_oracle_conv.restype = ctypes.c_int
+            lib.ssm_oracle_ckpt8.argtypes = [I64, I64] + [P] * 4
+            lib.ssm_oracle_ckpt8.restype = ctypes.c_int
             lib.ssm_oracle_max_threads.argtypes = []
             lib.ssm_oracle_max_threads.restype = ctypes.c_int
             _lib = lib
@@ -242,3 +246,87 @@ def dtproj(u, w, bias=None, g=None):
             raise RuntimeError("ssm_oracle_dtproj_bwd failed")
         res.update(du=du.reshape(*lead, R), dw=dw, dbias=dbias)
     return res
+
+
+def conv(x, w, bias=None, silu=True, s0=None, dy=None, dsL=None):
+    """Short causal convolution in float64: x, dy [B,L,D]; w [D,W]; bias [D]; s0, dsL [B,W-1,D].
+    Returns y and sL, and with ``dy`` also dx, dw, dbias, ds0 (see ssm_oracle.c)."""
+    lib = _load()
+    x, w = _f64(x), _f64(w)
+    B, L, D = x.shape
+    W = w.shape[1]
+    assert w.shape == (D, W)
+    bias, s0, dy, dsL = (None if a is None else _f64(a) for a in (bias, s0, dy, dsL))
+    for a, shape in ((bias, (D,)), (s0, (B, W - 1, D)), (dy, (B, L, D)), (dsL, (B, W - 1, D))):
+        assert a is None or a.shape == shape
+    out = {"y": np.full((B, L, D), np.nan), "sL": np.full((B, W - 1, D), np.nan)}
+    if dy is not None:
+        out.update(dx=np.full((B, L, D), np.nan), dw=np.full((D, W), np.nan),
+                   dbias=np.full((D,), np.nan), ds0=np.full((B, W - 1, D), np.nan))
+    rc = lib.ssm_oracle_conv(B, L, D, W, int(bool(silu)), _ptr(x), _ptr(w), _ptr(bias), _ptr(s0),
+                             _ptr(dy), _ptr(dsL), *(_ptr(out.get(k)) for k in
+                                                    ("y", "sL", "dx", "dw", "dbias", "ds0")))
+    if rc != 0:
+        raise RuntimeError("ssm_oracle_conv failed (bad argument or out of memory)")
+    return out
+
+
+def ckpt8(x):
+    """8-bit checkpoint of x [..., D]: (q int8, qe uint8 [..., ceil(D/32)], the values float64)."""
+    x = _f64(x)
+    D = x.shape[-1]
+    q = np.zeros(x.shape, np.int8)
+    qe = np.zeros((*x.shape[:-1], -(-D // 32)), np.uint8)
+    val = np.zeros(x.shape)
+    if _load().ssm_oracle_ckpt8(x.size // D, D, _ptr(x), _ptr(q), _ptr(qe), _ptr(val)) != 0:
+        raise RuntimeError("ssm_oracle_ckpt8 failed")
+    return q, qe, val
+
+
+def _serve(one, x, offsets, slot, pool, carry, y):
+    """Runs ``one(rows, state) -> (y rows, new state)`` over the sequences of a packed batch.  A
+    sequence that names an entry an earlier one names, or lies outside, is left out."""
+    y, pool = np.array(y, np.float64), np.array(pool, np.float64)
+    seen = set()
+    for s in range(len(slot)):
+        k, lo, hi = int(slot[s]), int(offsets[s]), int(offsets[s + 1])
+        if k >= len(pool) or k in seen or lo < 0 or hi < lo or hi > len(x):
+            continue
+        state = np.zeros(pool.shape[1:])
+        if k >= 0:
+            seen.add(k)
+            if carry is not None and carry[s]:
+                state = pool[k].copy()
+        y[lo:hi], state = one(slice(lo, hi), state)
+        if k >= 0:
+            pool[k] = state
+    return y, pool
+
+
+def conv_serve(x, w, bias, offsets, slot, pool, carry=None, silu=True, y=0.0):
+    """Convolution of packed prompts: x [R,D], pool [slots,W-1,D] -> (y [R,D], pool), float64; rows
+    of no sequence keep ``y``'s value."""
+    x = _f64(x)
+
+    def one(rows, state):
+        r = conv(x[rows][None], w, bias, silu, s0=state[None])
+        return r["y"][0], r["sL"][0]
+    return _serve(one, x, offsets, slot, pool, carry, np.broadcast_to(y, x.shape))
+
+
+def scan_serve(x, delta_raw, A_log, Bm, Cm, Dskip, offsets, slot, pool, carry=None, z=None,
+               zoh=False, y=0.0):
+    """Scan of packed prompts: x, delta_raw, z [R,D], Bm, Cm [R,N], pool [slots,D,N] -> (y, pool),
+    float64; with z, y is times z sigmoid(z)."""
+    x = _f64(x)
+
+    def one(rows, state):
+        r = real(x[rows][None], delta_raw[rows][None], A_log, Bm[rows][None], Cm[rows][None], Dskip,
+                 zoh=zoh, h0=state[None])
+        out = r["y"][0]
+        if z is not None:
+            v = _f64(z[rows])
+            e = np.exp(-np.abs(v))
+            out = out * v * np.where(v >= 0, 1 / (1 + e), e / (1 + e))
+        return out, r["hL"][0]
+    return _serve(one, x, offsets, slot, pool, carry, np.broadcast_to(y, x.shape))

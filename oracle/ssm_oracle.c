@@ -580,3 +580,106 @@ int ssm_oracle_dtproj_bwd(int64_t M, int64_t D, int64_t R, const double* u, cons
     }
     return 0;
 }
+
+/*
+ * Short causal convolution, one filter of W taps per channel:
+ *     v_t = bias + sum_j w[j] x_{t-(W-1)+j},  y_t = v_t sigmoid(v_t) (silu) or v_t,
+ * with x_{-(W-1)}..x_{-1} = s0 (NULL: zero) and sL the last W-1 entries of (s0, x).  With dy (and
+ * dsL, NULL: zero) the gradient of sum dy·y + sum dsL·sL, by the definition: every v_t gives
+ * g_t = dy_t dy_t/dv_t to its W inputs and taps.  x, y, dy, dx [B,L,D], s0, sL, dsL, ds0 [B,W-1,D],
+ * w, dw [D,W], bias, dbias [D]; all float64.
+ */
+int ssm_oracle_conv(int64_t B, int64_t L, int64_t D, int64_t W, int silu, const double* x,
+                    const double* w, const double* bias, const double* s0, const double* dy,
+                    const double* dsL, double* y, double* sL, double* dx, double* dw, double* dbias,
+                    double* ds0) {
+    if (B < 0 || L < 0 || D < 1 || W < 1 || !w || !y || !sL) return -1;
+    if (dy && (!dx || !dw || !dbias || !ds0)) return -1;
+    const int64_t P = W - 1;
+    int fail = 0;
+#pragma omp parallel for schedule(static)
+    for (int64_t d = 0; d < D; ++d) {
+        double* xp = calloc((size_t)(L + P + 1), sizeof(double));   /* (s0, x) of one channel */
+        double* gp = calloc((size_t)(L + P + 1), sizeof(double));   /* its gradient */
+        if (!xp || !gp) {
+#pragma omp atomic write
+            fail = 1;
+            free(xp); free(gp);
+            continue;
+        }
+        if (dy) {
+            for (int64_t j = 0; j < W; ++j) dw[d * W + j] = 0.0;
+            dbias[d] = 0.0;
+        }
+        for (int64_t b = 0; b < B; ++b) {
+            for (int64_t i = 0; i < P; ++i) xp[i] = s0 ? s0[(b * P + i) * D + d] : 0.0;
+            for (int64_t t = 0; t < L; ++t) xp[P + t] = x[(b * L + t) * D + d];
+            for (int64_t i = 0; i < L + P; ++i) gp[i] = 0.0;
+            for (int64_t t = 0; t < L; ++t) {
+                double v = bias ? bias[d] : 0.0;
+                for (int64_t j = 0; j < W; ++j) v += w[d * W + j] * xp[t + j];
+                const double s = sigmoid(v);
+                y[(b * L + t) * D + d] = silu ? v * s : v;
+                if (dy) {
+                    const double g = dy[(b * L + t) * D + d] * (silu ? s * (1.0 + v * (1.0 - s)) : 1.0);
+                    dbias[d] += g;
+                    for (int64_t j = 0; j < W; ++j) {
+                        dw[d * W + j] += g * xp[t + j];
+                        gp[t + j] += g * w[d * W + j];
+                    }
+                }
+            }
+            for (int64_t i = 0; i < P; ++i) {
+                sL[(b * P + i) * D + d] = xp[L + i];
+                if (dy && dsL) gp[L + i] += dsL[(b * P + i) * D + d];
+            }
+            if (dy) {
+                for (int64_t i = 0; i < P; ++i) ds0[(b * P + i) * D + d] = gp[i];
+                for (int64_t t = 0; t < L; ++t) dx[(b * L + t) * D + d] = gp[P + t];
+            }
+        }
+        free(xp); free(gp);
+    }
+    return fail ? -1 : 0;
+}
+
+/*
+ * 8-bit checkpoint of M rows of D values: groups of 32 share the step 2^(qe - 127), with a the
+ * group's largest magnitude 2^(floor(log2 a) - 6), twice that where a is nearer to 128 steps than to
+ * 127 (not from 2^127 on, where 127 is the limit), at least 2^-126; q = x / step rounded to nearest, ties to even.  All zero: qe 0; infinity or
+ * NaN in the group: qe 255, q 0.  val gets the values that q and qe stand for.
+ */
+int ssm_oracle_ckpt8(int64_t M, int64_t D, const double* x, int8_t* q, uint8_t* qe, double* val) {
+    if (M < 0 || D < 1 || !q || !qe || !val) return -1;
+    const int64_t G = (D + 31) / 32;
+    for (int64_t m = 0; m < M; ++m)
+        for (int64_t k = 0; k < G; ++k) {
+            const int64_t lo = k * 32, hi = lo + 32 < D ? lo + 32 : D;
+            double top = 0.0;
+            int finite = 1;
+            for (int64_t d = lo; d < hi; ++d) {
+                const double a = fabs(x[m * D + d]);
+                if (!isfinite(a)) finite = 0;
+                if (a > top) top = a;
+            }
+            int e = 0;
+            if (!finite) {
+                e = 255;
+            } else if (top > 0.0) {
+                int k2;
+                frexp(top, &k2);               /* top = f 2^k2, f in [0.5, 1) */
+                e = k2 - 1 - 6 + 127;
+                if (e < 1) e = 1;
+                if (e < 248 && ldexp(top, 127 - e) >= 127.5) ++e;
+            }
+            qe[m * G + k] = (uint8_t)e;
+            for (int64_t d = lo; d < hi; ++d) {
+                double r = e == 0 || e == 255 ? 0.0 : nearbyint(ldexp(x[m * D + d], 127 - e));
+                if (r > 127.0) r = 127.0;
+                if (r < -127.0) r = -127.0;
+                q[m * D + d] = (int8_t)r;
+                val[m * D + d] = e == 255 ? NAN : ldexp(r, e - 127);
+            }
+        }
+    return 0;
+}

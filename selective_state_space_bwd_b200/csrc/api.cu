@@ -1,14 +1,16 @@
 // C-ABI entry points (include/ssm_scan.h): argument validation on the host, workspace layout,
 // kernel launches.  Nothing here allocates memory or keeps state between calls.
 #include "../../include/ssm_scan.h"
+#include "api_util.h"
 #include "ssm_internal.h"
 
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+using namespace ssm_api;
+
 namespace {
 
-constexpr size_t kStatusBytes = 256;
 // The real backward keeps its scratch-slot mask in the status block, after the status word:
 // (kStatusBytes - kSlotMaskOffset) * 8 = 1984 slots at most.
 constexpr size_t kSlotMaskOffset = 32;
@@ -20,10 +22,6 @@ constexpr int64_t kRealFwdSplitCtas = 2368;
 // Also the number of scratch slots (window-start states, (delta, sigma)) of a launch with more
 // CTAs: a CTA holds one from its start to its end.
 constexpr int64_t kRealBwdSlots = 592;
-
-size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 bool valid_chunk(int T) { return T == 16 || T == 32 || T == 64 || T == 128 || T == 256; }
 
@@ -223,17 +221,6 @@ int plan_cplx(const ssm_cshape* s, CplxPlan* p) {
     return SSM_OK;
 }
 
-// A pointer may be null only when the array it describes is empty.
-bool ptr_ok(const void* ptr, size_t count) { return count == 0 || ptr != nullptr; }
-
-int check_arrays(const void* const* ptrs, const size_t* counts, int n) {
-    for (int i = 0; i < n; ++i) {
-        if (!ptr_ok(ptrs[i], counts[i])) return SSM_ERR_INVALID_ARG;
-        if (counts[i] && !aligned16(ptrs[i])) return SSM_ERR_MISALIGNED;
-    }
-    return SSM_OK;
-}
-
 int check_options(const ssm_scan_options& o) {
     if ((o.flags & ~SSM_FUSED_SUMS) != 0) return SSM_ERR_INVALID_ARG;
     if (o.discretization != SSM_EULER && o.discretization != SSM_ZOH) return SSM_ERR_INVALID_ARG;
@@ -246,11 +233,6 @@ int copy_or_zero(float* dst, const float* src, size_t n, cudaStream_t s) {
     const cudaError_t e = src ? cudaMemcpyAsync(dst, src, n * sizeof(float), cudaMemcpyDeviceToDevice, s)
                               : cudaMemsetAsync(dst, 0, n * sizeof(float), s);
     return e == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
-}
-
-template <typename T>
-T* at(void* ws, size_t off) {
-    return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
 }  // namespace

@@ -163,6 +163,82 @@ int64_t dtproj_rows_per_split(int R);
 cudaError_t launch_dtproj_fwd(const DtArgs& a, cudaStream_t st);
 cudaError_t launch_dtproj_bwd(const DtArgs& a, cudaStream_t st);
 
+// Short causal convolution (csrc/conv.cu).  A piece is G rows of one batch entry; a CTA takes ry
+// pieces of cx four-channel vectors; parts CTAs cover the nseg * B pieces, nct the channels.
+struct ConvArgs {
+    int B, L, D, G, nseg, parts, cx, ry, nct;
+    size_t ldx, ldy, lddy, lddx;
+    const void* x;
+    const int8_t* q;      // 8-bit checkpoint in (restore, backward)
+    const uint8_t* qe;
+    const float* w;
+    const float* bias;
+    const void* s0;
+    void* y;
+    void* sL;
+    int8_t* q_out;        // 8-bit checkpoint out (forward)
+    uint8_t* qe_out;
+    const void* dy;
+    const void* dsL;
+    void* dx;
+    void* ds0;
+    float* part;          // [parts][W+1][D] sums of dw and dbias
+    float* dw;
+    float* dbias;
+};
+void conv_plan(ConvArgs& a, bool backward);  // fills G, nseg, parts, cx, ry, nct from B, L, D
+cudaError_t launch_conv_fwd(const ConvArgs& a, int width, bool silu, int io_bf16, bool restore,
+                            cudaStream_t st);
+cudaError_t launch_conv_bwd(const ConvArgs& a, int width, bool silu, int io_bf16, cudaStream_t st);
+
+struct ConvServeArgs {
+    int rows, S, D, slots, G, cx, ry;
+    int64_t items;
+    size_t ldx, ldy;
+    const void* x;
+    const float* w;
+    const float* bias;
+    const int32_t* offsets;
+    const int32_t* slot;
+    const uint8_t* carry;
+    void* pool;
+    void* y;
+    unsigned* status;     // or null
+};
+cudaError_t launch_conv_prompt(ConvServeArgs a, int width, bool silu, int io_bf16, cudaStream_t st);
+cudaError_t launch_conv_step(const ConvServeArgs& a, int width, bool silu, int io_bf16, cudaStream_t st);
+
+// Scan over packed prompts and single tokens (csrc/serve_scan.cu).
+struct ScanServeArgs {
+    int rows, S, D, slots, max_len, zoh;
+    int G, split;         // rows a time segment; split: sequences of several segments may occur
+    int ndt;              // channel tiles
+    int64_t items;
+    size_t ldx, ldd, ldz, ldb, ldc, ldy;
+    const void* x;
+    const void* draw;
+    const float* A_log;
+    const void* Bm;
+    const void* Cm;
+    const float* Dskip;
+    const void* z;        // or null
+    const int32_t* offsets;
+    const int32_t* slot;
+    const uint8_t* carry;
+    float* pool;
+    void* y;
+    float* sumP;          // per item [items][D][N]: the segment's transition product, and its end
+    float* sumS;          //   state from zero, which the carry replaces by the state entering it
+    unsigned* status;     // or null
+};
+struct ScanServePlan {
+    int G, split, states; // states: states a thread owns
+    int64_t items;
+};
+ScanServePlan plan_scan_prompt(int64_t rows, int64_t S, int64_t D, int N, int64_t max_len);
+cudaError_t launch_scan_prompt(const ScanServeArgs& a, int io_bf16, int N, int states, cudaStream_t st);
+cudaError_t launch_scan_step(const ScanServeArgs& a, int io_bf16, int N, cudaStream_t st);
+
 // Launchers (return cudaGetLastError() of the last launch).
 cudaError_t launch_pdssm_fwd(const PdArgs& a, cudaStream_t st);
 cudaError_t launch_pdssm_bwd(const PdArgs& a, cudaStream_t st);

@@ -405,7 +405,8 @@ int ssm_dtproj_bwd(const ssm_dtshape* shape, const void* u, const void* w, const
  * ssm_conv_restore recomputes y (the scan's input) and ssm_conv_bwd takes its gradient, so that
  * neither x nor y has to be kept for the backward: 33/32 bytes an element.  In every row the 32
  * channels 32k..32k+31 (fewer at the end of the row) share one power of two: q[b,t,d] is an int8,
- * qe[b,t,k] a byte, and the value is q 2^(qe - 127).  With a the group's largest magnitude, the step
+ * qe[b,k,t] a byte, and the value is q 2^(qe - 127).  The bytes of one group lie along time, so that a
+ * thread walking down the rows reads four at once.  With a the group's largest magnitude, the step
  * is 2^(floor(log2 a) - 6), or twice that where a would round past 127, never below 2^-126; q is x
  * over the step rounded to nearest, ties to even, so a value is off by at most half a step (from
  * a = 2^127 on, where a larger step could not be restored, by less than one: 127 is the limit).  A
@@ -415,7 +416,8 @@ int ssm_dtproj_bwd(const ssm_dtshape* shape, const void* u, const void* w, const
  * Layout: x, y, dy, dx [B, L, D] in the io type, each with its own row stride (elements from one
  * step to the next; batch b starts L strides after batch b-1), so that one half of a projection's
  * [B, L, 2D] rows can be used in place; s0, sL, dsL, ds0 [B, W-1, D] dense, io type; w, dw [D, W] and
- * bias, dbias [D] fp32; q [B, L, D] int8 and qe [B, L, ceil(D/32)] bytes, dense.  Sums are
+ * bias, dbias [D] fp32; q [B, L, D] int8 and qe [B, ceil(D/32), L rounded up to a multiple of
+ * four] bytes, dense (what lies past L is written as zero, and not read).  Sums are
  * fp32; y, dx and ds0 are rounded to the io type once.  Outputs must not overlap inputs.
  */
 typedef struct ssm_conv_shape {

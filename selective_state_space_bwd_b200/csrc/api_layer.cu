@@ -47,7 +47,7 @@ ssm::ConvArgs conv_args(const ssm_conv_shape* s, bool backward) {
     a.B = (int)s->batch; a.L = (int)s->seqlen; a.D = (int)s->dim;
     a.ldx = stride(s->ldx, s->dim); a.ldy = stride(s->ldy, s->dim);
     a.lddy = stride(s->lddy, s->dim); a.lddx = stride(s->lddx, s->dim);
-    ssm::conv_plan(a, backward);
+    ssm::conv_plan(a, s->io == SSM_BF16, backward);
     return a;
 }
 
@@ -261,8 +261,8 @@ int ssm_conv_bwd(const ssm_conv_shape* shape, const void* x, const int8_t* q, co
     if (ds0 && (ds0 == s0 || ds0 == dsL)) return SSM_ERR_INVALID_ARG;
     if (ws_bytes < ssm_conv_workspace_bytes(shape)) return SSM_ERR_WORKSPACE_TOO_SMALL;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(ws, 0, sizeof(unsigned), s) != cudaSuccess) return SSM_ERR_CUDA;
     if (M == 0) {  // no steps: the state passes through, the sums are empty
+        if (cudaMemsetAsync(ws, 0, sizeof(unsigned), s) != cudaSuccess) return SSM_ERR_CUDA;
         if (cudaMemsetAsync(dw, 0, D * W * sizeof(float), s) != cudaSuccess) return SSM_ERR_CUDA;
         if (dbias && cudaMemsetAsync(dbias, 0, D * sizeof(float), s) != cudaSuccess) return SSM_ERR_CUDA;
         const size_t n = ds0 ? B * (W - 1) * D * esize(shape->io) : 0;
@@ -273,6 +273,7 @@ int ssm_conv_bwd(const ssm_conv_shape* shape, const void* x, const int8_t* q, co
     ssm::ConvArgs a = conv_args(shape, true);
     a.x = x; a.q = q; a.qe = qe; a.w = w; a.bias = bias; a.s0 = s0; a.dy = dy; a.dsL = dsL;
     a.dx = dx; a.dw = dw; a.dbias = dbias; a.ds0 = ds0;
+    a.status = at<unsigned>(ws, 0);
     a.part = at<float>(ws, kStatusBytes);
     return launch_status(ssm::launch_conv_bwd(a, shape->width, (shape->flags & SSM_CONV_SILU) != 0,
                                               shape->io == SSM_BF16, s));

@@ -1,70 +1,92 @@
 // Short causal convolution in front of the scan: forward, its recomputation from an 8-bit
 // checkpoint, its gradient, and the packed-prompt and single-token forms (include/ssm_scan.h).
 //
-// Every kernel is bound by memory traffic: 2 W + ~8 operations an element against 4 (forward, bf16)
-// to 6 bytes (backward).  A thread owns four consecutive channels (one fp32x2 pair each of two) and
-// walks down a piece of the rows, the last W-1 inputs in registers, so that an element is read once
-// from DRAM; the W-1 rows before a piece are read a second time (from L2).  Four channels, not
-// eight: the gradient keeps W taps, W+1 sums and two windows a channel, and at four channels two
-// CTAs of 256 threads stay resident.  A CTA is cx threads across (cx four-channel vectors, a multiple of
-// eight so that the eight lanes that share an 8-bit group's 32 channels are neighbours in a warp)
-// by ry pieces down; cx is D / 4 cut into equal column tiles of at most 32, so that a width just
-// past a tile leaves no tile empty.
+// Every kernel is bound by memory traffic, with the special-function unit (three operations for
+// two SiLUs) and, in the gradient, the fp32 pipes not far behind.  A thread owns V consecutive
+// channels and walks down a piece of the rows, the last W-1 inputs in registers, so that an element
+// is read once from DRAM (the W-1 rows before a piece a second time).  Each thread copies its
+// own rows into its own places of a ring in shared memory, kDepth groups of four rows ahead
+// (cp.async, 16 or 8 bytes): the bytes in flight, about 64 KB an SM, cost no registers, and since no other
+// thread reads them there is no barrier in the loop, only the thread's own wait_group.
+//
+// A CTA is cx threads across (a multiple of the 32 / V threads that share an 8-bit group's 32 channels, so
+// that they are neighbours in a warp) by ry pieces down; the channels are cut into equal tiles of at most
+// 32 threads, so that a width just past a tile leaves no tile empty.  The pieces are as long as one
+// wave of CTAs allows: long pieces read fewer rows twice and, in the gradient, leave fewer sums.
 #include "layer_common.cuh"
+#include "real_common.cuh"
+
+#include <type_traits>
 
 namespace ssm {
 namespace conv {
 namespace {
 
-constexpr int U = 4;  // rows whose loads are in flight ahead of the rows being computed
+constexpr int kThreads = 256;
+constexpr int kResident = 296;   // CTAs of a wave: two per SM (registers, and the ring)
+constexpr int U = 4;             // rows a group; row t of a piece that starts at t0 lies in slot (t - t0) % 4
 
-// cx multiples of 8 up to 32, ry = 256 / cx
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* smem_dst, const void* gmem_src) {
+    const unsigned s = (unsigned)__cvta_generic_to_shared(smem_dst);
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(gmem_src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(s), "l"(gmem_src), "n"(BYTES) : "memory");
+}
+using real::cp_async_commit;
+template <int PENDING>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(PENDING) : "memory");
+}
+
 struct Tile {
     int cx, ry, nct;
 };
-Tile tile_of(int D) {
-    const int nvec = (D + 31) / 32 * 8;
+Tile tile_of(int D, int V) {
+    const int grp = 32 / V;  // threads of 32 channels
+    const int nvec = (D + 31) / 32 * grp;
     Tile t;
     t.nct = (nvec + 31) / 32;
-    t.cx = ((nvec + t.nct - 1) / t.nct + 7) / 8 * 8;
-    t.ry = 256 / t.cx;
+    t.cx = ((nvec + t.nct - 1) / t.nct + grp - 1) / grp * grp;
+    t.ry = kThreads / t.cx;
     return t;
 }
 
-// The taps of four channels, tap-major: w[j][pair].
-template <int W>
-__device__ __forceinline__ void load_taps(float2 (&w)[W][2], float2 (&bias)[2], const float* pw,
+// The taps of V channels, tap-major: w[j][pair].
+template <int W, int V>
+__device__ __forceinline__ void load_taps(float2 (&w)[W][V / 2], float2 (&bias)[V / 2], const float* pw,
                                           const float* pb, int c) {
-    float f[4 * W];
+    float f[V * W];
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
+    for (int i = 0; i < V * W / 4; ++i) {
         const float4 v = __ldg(reinterpret_cast<const float4*>(pw + (size_t)c * W) + i);
         f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
     }
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-        w[j][0] = make_float2(f[j], f[W + j]);
-        w[j][1] = make_float2(f[2 * W + j], f[3 * W + j]);
+    for (int p = 0; p < V / 2; ++p) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][p] = make_float2(f[2 * p * W + j], f[(2 * p + 1) * W + j]);
+        bias[p] = pb ? __ldg(reinterpret_cast<const float2*>(pb + c) + p) : make_float2(0.f, 0.f);
     }
-    const float4 b = pb ? __ldg(reinterpret_cast<const float4*>(pb + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    bias[0] = make_float2(b.x, b.y);
-    bias[1] = make_float2(b.z, b.w);
 }
 
-template <int W>
-__device__ __forceinline__ void preact(float2 (&v)[2], const float2 (&w)[W][2],
-                                       const float2 (&bias)[2], const float2 (*x)[2]) {
+// The pre-activation of the row in slot u from the rows in the slots before it.
+template <int W, int P>
+__device__ __forceinline__ void preact(float2 (&v)[P], const float2 (&w)[W][P], const float2 (&bias)[P],
+                                       const float2 (&x)[U][P], int u) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
+    for (int p = 0; p < P; ++p) {
         v[p] = bias[p];
 #pragma unroll
-        for (int j = 0; j < W; ++j) v[p] = __ffma2_rn(w[j][p], x[j][p], v[p]);
+        for (int j = 0; j < W; ++j) v[p] = __ffma2_rn(w[j][p], x[(u + U - (W - 1) + j) % U][p], v[p]);
     }
 }
 
-__device__ __forceinline__ void silu4(float2 (&v)[2]) {
+template <int P>
+__device__ __forceinline__ void silu(float2 (&v)[P]) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p) v[p] = make_float2(silu_fast(v[p].x), silu_fast(v[p].y));
+    for (int p = 0; p < P; ++p) v[p] = silu_pair(v[p]);
 }
 
 // ---------------------------------------------------------------- 8-bit checkpoint
@@ -86,18 +108,17 @@ __device__ __forceinline__ unsigned step_exponent(unsigned top) {
 
 // Four int8 of x / 2^(qe - 127), rounded to nearest even: adding 1.5 * 2^23 leaves the rounded
 // integer in the low bits of the sum (the product by a power of two is exact).
-__device__ __forceinline__ unsigned quantise4(float2 (&x)[2], unsigned qe) {
+__device__ __forceinline__ unsigned quantise4(float2 x0, float2 x1, unsigned qe) {
     if (qe == 0u || qe == 255u) return 0u;
     const float f = __uint_as_float((254u - qe) << 23);
     if (qe == kTopStep) {
         const float m = 127.0f * __uint_as_float(kTopStep << 23);
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-            x[p] = make_float2(fminf(fmaxf(x[p].x, -m), m), fminf(fmaxf(x[p].y, -m), m));
+        x0 = make_float2(fminf(fmaxf(x0.x, -m), m), fminf(fmaxf(x0.y, -m), m));
+        x1 = make_float2(fminf(fmaxf(x1.x, -m), m), fminf(fmaxf(x1.y, -m), m));
     }
     const float magic = 12582912.0f;
-    const float2 a = __ffma2_rn(x[0], make_float2(f, f), make_float2(magic, magic));
-    const float2 b = __ffma2_rn(x[1], make_float2(f, f), make_float2(magic, magic));
+    const float2 a = __ffma2_rn(x0, make_float2(f, f), make_float2(magic, magic));
+    const float2 b = __ffma2_rn(x1, make_float2(f, f), make_float2(magic, magic));
     const unsigned lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
     const unsigned hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
     return __byte_perm(lo, hi, 0x5410);
@@ -105,7 +126,7 @@ __device__ __forceinline__ unsigned quantise4(float2 (&x)[2], unsigned qe) {
 
 // The values of four int8.  A byte u = q + 128 in the low bits of 2^23 is the float 2^23 + u; the
 // step of a NaN group (exponent 255) is infinite and its q zero, and 0 * inf is the NaN wanted.
-__device__ __forceinline__ void restore4(float2 (&x)[2], unsigned q, unsigned qe) {
+__device__ __forceinline__ void restore4(float2& x0, float2& x1, unsigned q, unsigned qe) {
     const float step = __uint_as_float(qe << 23);
     const unsigned u = q ^ 0x80808080u;
     const float off = -8388736.0f;  // -(2^23 + 128)
@@ -114,126 +135,183 @@ __device__ __forceinline__ void restore4(float2 (&x)[2], unsigned q, unsigned qe
                                  __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7541)));
     const float2 b = make_float2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7542)),
                                  __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7543)));
-    x[0] = __fmul2_rn(__fadd2_rn(a, o), s);
-    x[1] = __fmul2_rn(__fadd2_rn(b, o), s);
+    x0 = __fmul2_rn(__fadd2_rn(a, o), s);
+    x1 = __fmul2_rn(__fadd2_rn(b, o), s);
 }
 
 // ---------------------------------------------------------------- row sources
-// One row's four channels of one batch entry, from x or from its 8-bit checkpoint.
-template <typename E, bool Q8> struct Rows;
-template <typename E> struct Rows<E, false> {
-    using Raw = typename Quad<E>::Raw;
+// Rows of V channels of one batch entry, from x or from its 8-bit checkpoint.  word(t): the step
+// exponents of the four rows from t on (t a multiple of four), a byte a row; unused for x.
+template <typename E, int V, bool Q8> struct Rows;
+template <typename E, int V> struct Rows<E, V, false> {
+    using Raw = typename Vec<E, V>::Raw;
     const E* x;
     size_t ld;
     __device__ __forceinline__ Rows(const ConvArgs& a, int b, int c)
         : x(static_cast<const E*>(a.x) + (size_t)b * a.L * a.ldx + c), ld(a.ldx) {}
-    __device__ __forceinline__ Raw load(int t) const { return ld_quad(x + (size_t)t * ld); }
-    static __device__ __forceinline__ Raw zero() { return Quad<E>::zero(); }
-    static __device__ __forceinline__ void unpack(const Raw& r, float2 (&o)[2]) { Quad<E>::unpack(r, o); }
+    __device__ __forceinline__ const void* at(int t) const { return x + (size_t)t * ld; }
+    __device__ __forceinline__ unsigned word(int) const { return 0u; }
+    static __device__ __forceinline__ void unpack(const Raw& r, unsigned, float2 (&o)[V / 2]) {
+        Vec<E, V>::unpack(r, o);
+    }
+    __device__ __forceinline__ void load(int t, float2 (&o)[V / 2]) const {
+        Vec<E, V>::unpack(*static_cast<const Raw*>(at(t)), o);
+    }
 };
-template <typename E> struct Rows<E, true> {
-    struct Raw { unsigned q, e; };
+template <typename E> struct Rows<E, 4, true> {
+    using Raw = unsigned;
     const int8_t* q;
     const uint8_t* e;
-    size_t D, ng;
+    size_t D;
     __device__ __forceinline__ Rows(const ConvArgs& a, int b, int c)
-        : q(a.q + (size_t)b * a.L * a.D + c), e(a.qe + (size_t)b * a.L * ((a.D + 31) / 32) + c / 32),
-          D(a.D), ng((a.D + 31) / 32) {}
-    __device__ __forceinline__ Raw load(int t) const {
-        return Raw{*reinterpret_cast<const unsigned*>(q + (size_t)t * D), e[(size_t)t * ng]};
+        : q(a.q + (size_t)b * a.L * a.D + c),
+          e(a.qe + ((size_t)b * ((a.D + 31) / 32) + c / 32) * a.Lq), D(a.D) {}
+    __device__ __forceinline__ const void* at(int t) const { return q + (size_t)t * D; }
+    __device__ __forceinline__ unsigned word(int t) const { return *reinterpret_cast<const unsigned*>(e + t); }
+    static __device__ __forceinline__ void unpack(const Raw& r, unsigned e, float2 (&o)[2]) {
+        restore4(o[0], o[1], r, e);
     }
-    static __device__ __forceinline__ Raw zero() { return Raw{0u, 0u}; }
-    static __device__ __forceinline__ void unpack(const Raw& r, float2 (&o)[2]) { restore4(o, r.q, r.e); }
+    __device__ __forceinline__ void load(int t, float2 (&o)[2]) const {
+        restore4(o[0], o[1], *static_cast<const Raw*>(at(t)), e[t]);
+    }
+};
+template <typename E> struct Rows<E, 8, true> {
+    using Raw = uint2;
+    const int8_t* q;
+    const uint8_t* e;
+    size_t D;
+    __device__ __forceinline__ Rows(const ConvArgs& a, int b, int c)
+        : q(a.q + (size_t)b * a.L * a.D + c),
+          e(a.qe + ((size_t)b * ((a.D + 31) / 32) + c / 32) * a.Lq), D(a.D) {}
+    __device__ __forceinline__ const void* at(int t) const { return q + (size_t)t * D; }
+    __device__ __forceinline__ unsigned word(int t) const { return *reinterpret_cast<const unsigned*>(e + t); }
+    static __device__ __forceinline__ void unpack(const Raw& r, unsigned e, float2 (&o)[4]) {
+        restore4(o[0], o[1], r.x, e);
+        restore4(o[2], o[3], r.y, e);
+    }
+    __device__ __forceinline__ void load(int t, float2 (&o)[4]) const {
+        unpack(*static_cast<const Raw*>(at(t)), e[t], o);
+    }
 };
 
 // Row t < 0 of a sequence: the state before it, or zero.
-template <typename E, int W>
-__device__ __forceinline__ void past_row(float2 (&o)[2], const E* s0, int t, size_t D) {
-    if (s0)
-        Quad<E>::unpack(ld_quad(s0 + (size_t)(t + W - 1) * D), o);
-    else
-        o[0] = o[1] = make_float2(0.f, 0.f);
+template <typename E, int W, int V>
+__device__ __forceinline__ void past_row(float2 (&o)[V / 2], const E* s0, int t, size_t D) {
+    if (s0) {
+        Vec<E, V>::unpack(ld_vec<E, V>(s0 + (size_t)(t + W - 1) * D), o);
+    } else {
+#pragma unroll
+        for (int p = 0; p < V / 2; ++p) o[p] = make_float2(0.f, 0.f);
+    }
 }
 
 // ---------------------------------------------------------------- forward
 // SRC8: from the checkpoint (restore); DST8: write the checkpoint.
-template <typename E, int W, bool SILU, bool SRC8, bool DST8>
-__global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a) {
+template <typename E, int V, int W, bool SILU, bool SRC8, bool DST8>
+struct Fwd {
+    using R = Rows<E, V, SRC8>;
+    static constexpr int kDepth = sizeof(typename R::Raw) == 16 ? 3 : 4;
+    static constexpr int kBytes = kDepth * U * kThreads * (int)sizeof(typename R::Raw);
+};
+
+template <typename E, int V, int W, bool SILU, bool SRC8, bool DST8>
+__global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(ConvArgs a) {
+    using F = Fwd<E, V, W, SILU, SRC8, DST8>;
+    using R = typename F::R;
+    using Raw = typename R::Raw;
+    constexpr int P = V / 2, DEPTH = F::kDepth;
+    extern __shared__ __align__(16) unsigned char smem[];
+    Raw* ring = reinterpret_cast<Raw*>(smem) + threadIdx.x;  // slot k: ring[k * kThreads]
     const int tx = threadIdx.x % a.cx, ty = threadIdx.x / a.cx;
     const int64_t piece = (int64_t)blockIdx.x * a.ry + ty;
-    if (piece >= (int64_t)a.B * a.nseg) return;  // whole rows of threads: whole groups of eight lanes
-    const int c = (blockIdx.y * a.cx + tx) * 4;
+    if (ty >= a.ry || piece >= (int64_t)a.B * a.nseg) return;  // whole rows of threads: whole 8-bit groups
+    const int c = (blockIdx.y * a.cx + tx) * V;
     const bool cv = c < a.D;
     const int b = (int)(piece / a.nseg), seg = (int)(piece % a.nseg);
     const int t0 = seg * a.G, t1 = min(a.L, t0 + a.G);
     if (!DST8 && !cv) return;
     const int cc = cv ? c : 0;  // lanes past the last channel only take part in the group's maximum
 
-    float2 w[W][2], bias[2];
-    load_taps<W>(w, bias, a.w, a.bias, cc);
-    const Rows<E, SRC8> rows(a, b, cc);
-    const E* s0 = a.s0 ? static_cast<const E*>(a.s0) + (size_t)b * (W - 1) * a.D + cc : nullptr;
-    E* y = static_cast<E*>(a.y) + (size_t)b * a.L * a.ldy + cc;
-    const int ng = (a.D + 31) / 32;
+    const R rows(a, b, cc);
+    auto issue = [&](int t, int stage) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t + u < t1) cp_async<sizeof(Raw)>(ring + (stage * U + u) * kThreads, rows.at(t + u));
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < DEPTH - 1; ++s) issue(t0 + s * U, s);
+    unsigned ew = SRC8 && t0 < t1 ? rows.word(t0) : 0u;
 
-    using R = Rows<E, SRC8>;
-    typename R::Raw raw[U];
+    float2 w[W][P], bias[P], x[U][P];
+    load_taps<W, V>(w, bias, a.w, a.bias, cc);
+    const E* s0 = a.s0 ? static_cast<const E*>(a.s0) + (size_t)b * (W - 1) * a.D + cc : nullptr;
 #pragma unroll
-    for (int u = 0; u < U; ++u) raw[u] = t0 + u < t1 && cv ? rows.load(t0 + u) : R::zero();
-    float2 x[W - 1 + U][2];  // x[W-1+u] is row t+u
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        const int t = t0 - (W - 1) + j;
-        if (t < 0)
-            past_row<E, W>(x[j], s0, t, a.D);
+    for (int j = 1; j < W; ++j) {
+        if (t0 - j < 0)
+            past_row<E, W, V>(x[U - j], s0, t0 - j, a.D);
         else
-            R::unpack(rows.load(t), x[j]);
+            rows.load(t0 - j, x[U - j]);
     }
+    E* y = static_cast<E*>(a.y) + ((size_t)b * a.L + t0) * a.ldy + cc;
+    size_t qo = DST8 ? ((size_t)b * a.L + t0) * a.D + cc : 0;
+    int stage = 0;
     for (int t = t0; t < t1; t += U) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            R::unpack(raw[u], x[W - 1 + u]);
-            raw[u] = t + U + u < t1 && cv ? rows.load(t + U + u) : R::zero();
-        }
+        issue(t + (DEPTH - 1) * U, stage == 0 ? DEPTH - 1 : stage - 1);
+        unsigned en = 0u;
+        if (SRC8 && t + U < t1) en = rows.word(t + U);
+        cp_async_wait<DEPTH - 1>();
+        unsigned steps = 0u;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (t + u >= t1) break;
-            float2 v[2];
-            preact<W>(v, w, bias, &x[u]);
-            if (SILU) silu4(v);
-            if (cv) st_quad(y + (size_t)(t + u) * a.ldy, v);
+            R::unpack(ring[(stage * U + u) * kThreads], (ew >> (8 * u)) & 255u, x[u]);
+            float2 v[P];
+            preact<W, P>(v, w, bias, x, u);
+            if (SILU) silu<P>(v);
+            if (cv) st_vec<E, V>(y, v);
+            y += a.ldy;
             if (DST8) {
-                float2 q[2] = {x[W - 1 + u][0], x[W - 1 + u][1]};
-                const unsigned m = 0x7fffffffu;
-                unsigned top = max(max(__float_as_uint(q[0].x) & m, __float_as_uint(q[0].y) & m),
-                                   max(__float_as_uint(q[1].x) & m, __float_as_uint(q[1].y) & m));
-                const unsigned grp = 0xffu << (threadIdx.x & 24);
-                top = max(top, __shfl_xor_sync(grp, top, 1));
-                top = max(top, __shfl_xor_sync(grp, top, 2));
-                top = max(top, __shfl_xor_sync(grp, top, 4));
+                unsigned top = 0u;
+                if (cv) {
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        top = max(top, max(__float_as_uint(x[u][p].x) & 0x7fffffffu,
+                                           __float_as_uint(x[u][p].y) & 0x7fffffffu));
+                }
+                constexpr int GL = 32 / V;  // lanes of a group
+                const unsigned grp = ((1u << GL) - 1u) << (threadIdx.x & (32 - GL));
+#pragma unroll
+                for (int m = 1; m < GL; m <<= 1) top = max(top, __shfl_xor_sync(grp, top, m));
                 const unsigned e = step_exponent(top);
-                const size_t r = (size_t)b * a.L + t + u;
-                if (cv) *reinterpret_cast<unsigned*>(a.q_out + r * a.D + c) = quantise4(q, e);
-                if (cv && (c & 31) == 0) a.qe_out[r * ng + c / 32] = (uint8_t)e;
+                steps |= e << (8 * u);
+                if (cv) {
+                    if constexpr (V == 4)
+                        *reinterpret_cast<unsigned*>(a.q_out + qo) = quantise4(x[u][0], x[u][1], e);
+                    else
+                        *reinterpret_cast<uint2*>(a.q_out + qo) =
+                            make_uint2(quantise4(x[u][0], x[u][1], e), quantise4(x[u][P - 2], x[u][P - 1], e));
+                }
+                qo += a.D;
             }
         }
-        if (t + U <= t1) {
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) { x[j][0] = x[U + j][0]; x[j][1] = x[U + j][1]; }
-        }
+        if (DST8 && cv && (c & 31) == 0)
+            *reinterpret_cast<unsigned*>(a.qe_out + ((size_t)b * ((a.D + 31) / 32) + c / 32) * a.Lq + t) = steps;
+        ew = en;
+        stage = stage == DEPTH - 1 ? 0 : stage + 1;
     }
-    if (a.sL && cv && t1 == a.L && seg == a.nseg - 1) {
+    if (a.sL && cv && seg == a.nseg - 1) {
         // the last W-1 inputs, read again: the window's place depends on the length
         E* sL = static_cast<E*>(a.sL) + (size_t)b * (W - 1) * a.D + c;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const int t = a.L - (W - 1) + j;
-            float2 v[2];
+            float2 v[P];
             if (t < 0)
-                past_row<E, W>(v, s0, t, a.D);
+                past_row<E, W, V>(v, s0, t, a.D);
             else
-                R::unpack(rows.load(t), v);
-            st_quad(sL + (size_t)j * a.D, v);
+                rows.load(t, v);
+            st_vec<E, V>(sL + (size_t)j * a.D, v);
         }
     }
 }
@@ -241,10 +319,28 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a) {
 // ---------------------------------------------------------------- backward
 // A piece's own rows t0..t1-1 give the sums of dw and dbias; dx_t needs g up to t + W-1, so the
 // walk goes on for W-1 rows past the piece (g recomputed, not summed) and emits dx W-1 rows behind
-// itself.  Past the end g is zero; before the start the rows are s0's.
+// itself.  Past the end g is zero; before the start the rows are s0's.  Four channels a thread: W
+// taps, W+1 sums and the two windows are 60 registers, and two CTAs stay resident.
+template <typename E, bool SRC8>
+struct Bwd {
+    using R = Rows<E, 4, SRC8>;
+    using Raw = typename R::Raw;
+    using GRaw = typename Vec<E, 4>::Raw;
+    static constexpr int kPer = U * kThreads * (int)(sizeof(Raw) + sizeof(GRaw));
+    static constexpr int kDepth = kPer <= 12288 ? 4 : (kPer <= 16384 ? 3 : 2);
+    static constexpr int kBytes = kDepth * kPer;  // the sums at the end, 20 KB, reuse it
+};
+
 template <typename E, int W, bool SILU, bool SRC8>
-__global__ void __launch_bounds__(256, 2) conv_bwd_kernel(ConvArgs a) {
-    __shared__ float red[256 * 4];
+__global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
+    using Cfg = Bwd<E, SRC8>;
+    using R = typename Cfg::R;
+    using Raw = typename Cfg::Raw;
+    using GRaw = typename Cfg::GRaw;
+    constexpr int DEPTH = Cfg::kDepth;
+    extern __shared__ __align__(16) unsigned char smem[];
+    GRaw* gring = reinterpret_cast<GRaw*>(smem) + threadIdx.x;
+    Raw* xring = reinterpret_cast<Raw*>(smem + DEPTH * U * kThreads * sizeof(GRaw)) + threadIdx.x;
     const int tx = threadIdx.x % a.cx, ty = threadIdx.x / a.cx;
     const int64_t piece = (int64_t)blockIdx.x * a.ry + ty;
     const int c = (blockIdx.y * a.cx + tx) * 4;
@@ -252,128 +348,136 @@ __global__ void __launch_bounds__(256, 2) conv_bwd_kernel(ConvArgs a) {
 #pragma unroll
     for (int j = 0; j <= W; ++j) sum[j][0] = sum[j][1] = make_float2(0.f, 0.f);
 
-    if (piece < (int64_t)a.B * a.nseg && c < a.D) {
+    if (ty < a.ry && piece < (int64_t)a.B * a.nseg && c < a.D) {
         const int b = (int)(piece / a.nseg), seg = (int)(piece % a.nseg);
         const int t0 = seg * a.G, t1 = min(a.L, t0 + a.G);
-        float2 w[W][2], bias[2];
-        load_taps<W>(w, bias, a.w, a.bias, c);
-        using R = Rows<E, SRC8>;
+        const int tend = min(a.L, t1 + W - 1);  // rows with a gradient that this piece needs
+        const int lo = t0 > 0 ? t0 : -(W - 1);  // rows whose gradient this piece writes: lo..t1-1
         const R rows(a, b, c);
+        const E* dy = static_cast<const E*>(a.dy) + (size_t)b * a.L * a.lddy + c;
+        auto issue = [&](int t, int stage) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (t + u < tend) {
+                    cp_async<sizeof(GRaw)>(gring + (stage * U + u) * kThreads, dy + (size_t)(t + u) * a.lddy);
+                    cp_async<sizeof(Raw)>(xring + (stage * U + u) * kThreads, rows.at(t + u));
+                }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int s = 0; s < DEPTH - 1; ++s) issue(t0 + s * U, s);
+        unsigned ew = SRC8 && t0 < tend ? rows.word(t0) : 0u;
+
+        float2 w[W][2], bias[2], x[U][2], g[U][2];
+        load_taps<W, 4>(w, bias, a.w, a.bias, c);
         const size_t so = (size_t)b * (W - 1) * a.D + c;
         const E* s0 = a.s0 ? static_cast<const E*>(a.s0) + so : nullptr;
         const E* dsL = a.dsL ? static_cast<const E*>(a.dsL) + so : nullptr;
         E* ds0 = a.ds0 ? static_cast<E*>(a.ds0) + so : nullptr;
-        const E* dy = static_cast<const E*>(a.dy) + (size_t)b * a.L * a.lddy + c;
         E* dx = static_cast<E*>(a.dx) + (size_t)b * a.L * a.lddx + c;
-        const int tend = min(a.L, t1 + W - 1);  // rows with a gradient that this piece needs
-        const int lo = t0 > 0 ? t0 : -(W - 1);  // rows whose gradient this piece writes: lo..t1-1
-
-        typename R::Raw rx[U];
-        typename Quad<E>::Raw rg[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            rx[u] = t0 + u < tend ? rows.load(t0 + u) : R::zero();
-            rg[u] = t0 + u < tend ? ld_quad(dy + (size_t)(t0 + u) * a.lddy) : Quad<E>::zero();
-        }
-        float2 x[W - 1 + U][2];  // x[W-1+u] is row t+u
-        float2 g[W - 1 + U][2];  // g[W-1+u] is row t+u
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-            const int t = t0 - (W - 1) + j;
-            if (t < 0)
-                past_row<E, W>(x[j], s0, t, a.D);
+        for (int j = 1; j < W; ++j) {
+            if (t0 - j < 0)
+                past_row<E, W, 4>(x[U - j], s0, t0 - j, a.D);
             else
-                R::unpack(rows.load(t), x[j]);
-            g[j][0] = g[j][1] = make_float2(0.f, 0.f);
+                rows.load(t0 - j, x[U - j]);
+            g[U - j][0] = g[U - j][1] = make_float2(0.f, 0.f);
         }
-        for (int t = t0; t < t1 + W - 1; t += U) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                R::unpack(rx[u], x[W - 1 + u]);
-                Quad<E>::unpack(rg[u], g[W - 1 + u]);
-                const int tn = t + U + u;
-                rx[u] = tn < tend ? rows.load(tn) : R::zero();
-                rg[u] = tn < tend ? ld_quad(dy + (size_t)tn * a.lddy) : Quad<E>::zero();
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float2 (&gu)[2] = g[W - 1 + u];  // dy, now to become dL/dv
-                if (SILU) {
-                    float2 v[2];
-                    preact<W>(v, w, bias, &x[u]);
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const float2 s = make_float2(__fdividef(1.0f, 1.0f + ex2_mufu(-v[p].x * kLog2e)),
-                                                     __fdividef(1.0f, 1.0f + ex2_mufu(-v[p].y * kLog2e)));
-                        // d (v s) / dv = s + v s (1 - s)
-                        const float2 one = make_float2(1.f, 1.f);
-                        const float2 r = __ffma2_rn(s, make_float2(-1.f, -1.f), one);
-                        gu[p] = __fmul2_rn(gu[p], __fmul2_rn(s, __ffma2_rn(v[p], r, one)));
-                    }
-                }
-                if (t + u >= tend) gu[0] = gu[1] = make_float2(0.f, 0.f);
-                if (t + u < t1) {
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-#pragma unroll
-                        for (int j = 0; j < W; ++j) sum[j][p] = __ffma2_rn(gu[p], x[u + j][p], sum[j][p]);
-                        sum[W][p] = __fadd2_rn(sum[W][p], gu[p]);
-                    }
-                }
-                const int r = t + u - (W - 1);  // the row whose last contribution this is
-                if (r < lo || r >= t1) continue;
-                float2 d[2];
+        // one row: INNER when it is summed, writes a row of dx, and nothing touches the ends
+        auto row = [&](int t, int u, int stage, auto inner) {
+            constexpr bool INNER = decltype(inner)::value;
+            R::unpack(xring[(stage * U + u) * kThreads], (ew >> (8 * u)) & 255u, x[u]);
+            Vec<E, 4>::unpack(gring[(stage * U + u) * kThreads], g[u]);  // dy, now to become dL/dv
+            if (SILU) {
+                float2 v[2];
+                preact<W, 2>(v, w, bias, x, u);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    d[p] = __fmul2_rn(w[W - 1][p], g[u][p]);
-#pragma unroll
-                    for (int k = 1; k < W; ++k) d[p] = __ffma2_rn(w[W - 1 - k][p], g[u + k][p], d[p]);
+                    // d (v s) / dv = s (1 + v (1 - s)), with 1 - s = e s exact where s is next to 1
+                    float2 s, e;
+                    sigmoid_pair(v[p], s, e);
+                    g[u][p] = __fmul2_rn(g[u][p], __fmul2_rn(s, __ffma2_rn(v[p], __fmul2_rn(e, s),
+                                                                            make_float2(1.f, 1.f))));
                 }
-                if (dsL && r >= a.L - (W - 1)) {
-                    float2 e[2];
-                    Quad<E>::unpack(ld_quad(dsL + (size_t)(r - (a.L - (W - 1))) * a.D), e);
-                    d[0] = __fadd2_rn(d[0], e[0]);
-                    d[1] = __fadd2_rn(d[1], e[1]);
-                }
-                if (r >= 0)
-                    st_quad(dx + (size_t)r * a.lddx, d);
-                else if (ds0)
-                    st_quad(ds0 + (size_t)(r + W - 1) * a.D, d);
             }
+            if (!INNER && t >= tend) g[u][0] = g[u][1] = make_float2(0.f, 0.f);  // the ring holds other rows
+            if (INNER || t < t1) {
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) {
-                x[j][0] = x[U + j][0]; x[j][1] = x[U + j][1];
-                g[j][0] = g[U + j][0]; g[j][1] = g[U + j][1];
+                for (int p = 0; p < 2; ++p) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        sum[j][p] = __ffma2_rn(g[u][p], x[(u + U - (W - 1) + j) % U][p], sum[j][p]);
+                    sum[W][p] = __fadd2_rn(sum[W][p], g[u][p]);
+                }
             }
+            const int r = t - (W - 1);  // the row whose last contribution this is
+            if (!INNER && (r < lo || r >= t1)) return;
+            float2 d[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                d[p] = __fmul2_rn(w[W - 1][p], g[(u + U - (W - 1)) % U][p]);
+#pragma unroll
+                for (int k = 1; k < W; ++k)
+                    d[p] = __ffma2_rn(w[W - 1 - k][p], g[(u + U - (W - 1) + k) % U][p], d[p]);
+            }
+            if (!INNER && dsL && r >= a.L - (W - 1)) {
+                float2 e[2];
+                Vec<E, 4>::unpack(ld_vec<E, 4>(dsL + (size_t)(r - (a.L - (W - 1))) * a.D), e);
+                d[0] = __fadd2_rn(d[0], e[0]);
+                d[1] = __fadd2_rn(d[1], e[1]);
+            }
+            if (INNER || r >= 0)
+                st_vec<E, 4>(dx + (size_t)r * a.lddx, d);
+            else if (ds0)
+                st_vec<E, 4>(ds0 + (size_t)(r + W - 1) * a.D, d);
+        };
+        int stage = 0;
+        for (int t = t0; t < t1 + W - 1; t += U) {
+            issue(t + (DEPTH - 1) * U, stage == 0 ? DEPTH - 1 : stage - 1);
+            unsigned en = 0u;
+            if (SRC8 && t + U < tend) en = rows.word(t + U);
+            cp_async_wait<DEPTH - 1>();
+            if (t > t0 && t + U <= t1) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) row(t + u, u, stage, std::true_type{});
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) row(t + u, u, stage, std::false_type{});
+            }
+            ew = en;
+            stage = stage == DEPTH - 1 ? 0 : stage + 1;
         }
     }
-    // the CTA's sums over its ry pieces, in their order, one tap at a time
-#pragma unroll 1
-    for (int j = 0; j <= W; ++j) {
-        float2 s[2] = {sum[0][0], sum[0][1]};
+    // the CTA's sums over its ry pieces, in their order
+    cp_async_wait<0>();
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(smem);  // [W+1][ry][cx * 4]
+    const int wid = a.cx * 4;
+    if (ty < a.ry) {
 #pragma unroll
-        for (int k = 1; k <= W; ++k)
-            if (k == j) { s[0] = sum[k][0]; s[1] = sum[k][1]; }
-        __syncthreads();
-        *reinterpret_cast<float4*>(red + threadIdx.x * 4) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
-        __syncthreads();
-        for (int i = threadIdx.x; i < a.cx * 4; i += blockDim.x) {
-            const int ch = blockIdx.y * a.cx * 4 + i;
-            if (ch >= a.D) continue;
-            float v = 0.f;
-            for (int k = 0; k < a.ry; ++k) v += red[k * a.cx * 4 + i];
-            a.part[((size_t)blockIdx.x * (W + 1) + j) * a.D + ch] = v;
-        }
+        for (int j = 0; j <= W; ++j)
+            *reinterpret_cast<float4*>(red + (j * a.ry + ty) * wid + tx * 4) =
+                make_float4(sum[j][0].x, sum[j][0].y, sum[j][1].x, sum[j][1].y);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < (W + 1) * wid; i += kThreads) {
+        const int j = i / wid, k = i - j * wid, ch = blockIdx.y * wid + k;
+        if (ch >= a.D) continue;
+        float v = 0.f;
+        for (int r = 0; r < a.ry; ++r) v += red[(j * a.ry + r) * wid + k];
+        a.part[((size_t)blockIdx.x * (W + 1) + j) * a.D + ch] = v;
     }
 }
 
 // dw and dbias from the CTAs' sums: 32 channels of one tap across, 8 shares of the CTAs down,
-// added in a fixed order.
+// added in a fixed order.  Its first thread writes the status word: nothing in the gradient can
+// fail on the device.
 __global__ void __launch_bounds__(256) conv_reduce_kernel(const float* part, int parts, int D, int W,
-                                                          float* dw, float* dbias) {
+                                                          float* dw, float* dbias, unsigned* status) {
     __shared__ float red[8][32];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + tx, j = blockIdx.y;
+    if (blockIdx.x == 0 && j == 0 && threadIdx.x == 0) *status = 0u;
     float s = 0.f;
     if (c < D)
         for (int k = ty; k < parts; k += 8) s += part[((size_t)k * (W + 1) + j) * D + c];
@@ -394,12 +498,16 @@ __global__ void __launch_bounds__(256) conv_reduce_kernel(const float* part, int
 // the state that it leaves belong to the same pool entry: the thread that reads the old one (the
 // sequence's first piece) also writes the new one, from x, so that no other thread of the launch
 // touches the entry.
-template <typename E, int W, bool SILU>
-__global__ void __launch_bounds__(256) conv_prompt_kernel(ConvServeArgs a) {
-    __shared__ int repeated[32];
+template <typename E, int V, int W, bool SILU>
+__global__ void __launch_bounds__(kThreads, 2) conv_prompt_kernel(ConvServeArgs a) {
+    using Raw = typename Vec<E, V>::Raw;
+    constexpr int P = V / 2, DEPTH = Fwd<E, V, W, SILU, false, false>::kDepth;
+    extern __shared__ __align__(16) unsigned char smem[];
+    Raw* ring = reinterpret_cast<Raw*>(smem) + threadIdx.x;
+    __shared__ int repeated[kThreads / 4 + 1];
     const int tx = threadIdx.x % a.cx, ty = threadIdx.x / a.cx;
     const int64_t item0 = (int64_t)blockIdx.x * a.ry, item = item0 + ty;
-    if (threadIdx.x < 32) repeated[threadIdx.x] = 0;
+    if (threadIdx.x <= kThreads / 4) repeated[threadIdx.x] = 0;
     if (a.status && blockIdx.x == 0 && blockIdx.y == 0)
         check_batch(a.offsets, a.slot, a.S, a.rows, a.slots, a.rows, a.status);
     int s = find_seq(a.offsets, a.S, a.G, item0);
@@ -413,60 +521,68 @@ __global__ void __launch_bounds__(256) conv_prompt_kernel(ConvServeArgs a) {
         if (tx == 0) flag_if(a.status, kStatusInvalid);
         return;
     }
-    const int c = (blockIdx.y * a.cx + tx) * 4;
+    const int c = (blockIdx.y * a.cx + tx) * V;
     if (c >= a.D) return;
     const int t0 = sp.first, t1 = min(sp.end, t0 + a.G);
     const E* xr = static_cast<const E*>(a.x) + c;
-    E* y = static_cast<E*>(a.y) + c;
-    typename Quad<E>::Raw raw[U];
+    auto issue = [&](int t, int stage) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) raw[u] = t0 + u < t1 ? ld_quad(xr + (size_t)(t0 + u) * a.ldx) : Quad<E>::zero();
-    float2 w[W][2], bias[2];
-    load_taps<W>(w, bias, a.w, a.bias, c);
-    float2 x[W - 1 + U][2];
+        for (int u = 0; u < U; ++u)
+            if (t + u < t1) cp_async<sizeof(Raw)>(ring + (stage * U + u) * kThreads, xr + (size_t)(t + u) * a.ldx);
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < DEPTH - 1; ++k) issue(t0 + k * U, k);
+    float2 w[W][P], bias[P], x[U][P];
+    load_taps<W, V>(w, bias, a.w, a.bias, c);
     E* entry = sp.slot >= 0 ? static_cast<E*>(a.pool) + (size_t)sp.slot * (W - 1) * a.D + c : nullptr;
     if (sp.local == 0) {
         const bool carry = entry && a.carry && a.carry[sp.s];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-            x[j][0] = x[j][1] = make_float2(0.f, 0.f);
-            if (carry) Quad<E>::unpack(ld_quad(entry + (size_t)j * a.D), x[j]);
+        for (int j = 0; j < W - 1; ++j) {  // entry j is input j - (W-1): slot U - (W-1) + j
+            float2 (&o)[P] = x[U - (W - 1) + j];
+#pragma unroll
+            for (int p = 0; p < P; ++p) o[p] = make_float2(0.f, 0.f);
+            if (carry) Vec<E, V>::unpack(ld_vec<E, V>(entry + (size_t)j * a.D), o);
         }
         if (entry) {
-            // entry i is input len + i - (W-1) of [past, x]: one of x, or of the W-1 in registers
+            // entry i becomes input len + i of [past, x]: one of x, or one of the W-1 in registers
             const int len = sp.end - t0;
 #pragma unroll
             for (int i = 0; i < W - 1; ++i) {
-                const int k = len + i;  // index into [past, x]
-                float2 v[2] = {x[0][0], x[0][1]};
+                const int k = len + i;
+                float2 v[P];
 #pragma unroll
-                for (int j = 1; j < W - 1; ++j)
-                    if (k == j) { v[0] = x[j][0]; v[1] = x[j][1]; }
-                if (k >= W - 1) Quad<E>::unpack(ld_quad(xr + (size_t)(t0 + k - (W - 1)) * a.ldx), v);
-                st_quad(entry + (size_t)i * a.D, v);
+                for (int p = 0; p < P; ++p) {
+                    v[p] = x[U - (W - 1)][p];
+#pragma unroll
+                    for (int j = 1; j < W - 1; ++j)
+                        if (k == j) v[p] = x[U - (W - 1) + j][p];
+                }
+                if (k >= W - 1) Vec<E, V>::unpack(ld_vec<E, V>(xr + (size_t)(t0 + k - (W - 1)) * a.ldx), v);
+                st_vec<E, V>(entry + (size_t)i * a.D, v);
             }
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-            Quad<E>::unpack(ld_quad(xr + (size_t)(t0 - (W - 1) + j) * a.ldx), x[j]);
+        for (int j = 1; j < W; ++j) Vec<E, V>::unpack(ld_vec<E, V>(xr + (size_t)(t0 - j) * a.ldx), x[U - j]);
     }
+    E* y = static_cast<E*>(a.y) + (size_t)t0 * a.ldy + c;
+    int stage = 0;
     for (int t = t0; t < t1; t += U) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            Quad<E>::unpack(raw[u], x[W - 1 + u]);
-            raw[u] = t + U + u < t1 ? ld_quad(xr + (size_t)(t + U + u) * a.ldx) : Quad<E>::zero();
-        }
+        issue(t + (DEPTH - 1) * U, stage == 0 ? DEPTH - 1 : stage - 1);
+        cp_async_wait<DEPTH - 1>();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (t + u >= t1) break;
-            float2 v[2];
-            preact<W>(v, w, bias, &x[u]);
-            if (SILU) silu4(v);
-            st_quad(y + (size_t)(t + u) * a.ldy, v);
+            Vec<E, V>::unpack(ring[(stage * U + u) * kThreads], x[u]);
+            float2 v[P];
+            preact<W, P>(v, w, bias, x, u);
+            if (SILU) silu<P>(v);
+            st_vec<E, V>(y, v);
+            y += a.ldy;
         }
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) { x[j][0] = x[U + j][0]; x[j][1] = x[U + j][1]; }
+        stage = stage == DEPTH - 1 ? 0 : stage + 1;
     }
 }
 
@@ -479,13 +595,13 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvServeArgs a) {
     const bool use = k >= 0 && k < a.slots;
     const bool work = use && c < a.D;
     E* entry = static_cast<E*>(a.pool) + (size_t)(use ? k : 0) * (W - 1) * a.D + c;
-    typename Quad<E>::Raw raw[W];
+    typename Vec<E, 4>::Raw raw[W];
 #pragma unroll
-    for (int j = 0; j < W; ++j) raw[j] = Quad<E>::zero();
+    for (int j = 0; j < W; ++j) raw[j] = Vec<E, 4>::zero();
     if (work) {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) raw[j] = ld_quad(entry + (size_t)j * a.D);
-        raw[W - 1] = ld_quad(static_cast<const E*>(a.x) + (size_t)row * a.ldx + c);
+        for (int j = 0; j < W - 1; ++j) raw[j] = ld_vec<E, 4>(entry + (size_t)j * a.D);
+        raw[W - 1] = ld_vec<E, 4>(static_cast<const E*>(a.x) + (size_t)row * a.ldx + c);
     }
     const bool repeated = a.slot && __syncthreads_or(named_before(a.slot, row, use ? k : -1, threadIdx.x, blockDim.x));
     if (k >= a.slots || repeated) {
@@ -493,16 +609,16 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvServeArgs a) {
         return;
     }
     if (!work) return;
-    float2 w[W][2], bias[2], x[W][2], v[2];
-    load_taps<W>(w, bias, a.w, a.bias, c);
+    float2 w[W][2], bias[2], x[U][2], v[2];
+    load_taps<W, 4>(w, bias, a.w, a.bias, c);
 #pragma unroll
-    for (int j = 0; j < W; ++j) Quad<E>::unpack(raw[j], x[j]);
+    for (int j = 0; j < W; ++j) Vec<E, 4>::unpack(raw[j], x[U - W + j]);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-        *reinterpret_cast<typename Quad<E>::Raw*>(entry + (size_t)j * a.D) = raw[j + 1];
-    preact<W>(v, w, bias, x);
-    if (SILU) silu4(v);
-    st_quad(static_cast<E*>(a.y) + (size_t)row * a.ldy + c, v);
+        *reinterpret_cast<typename Vec<E, 4>::Raw*>(entry + (size_t)j * a.D) = raw[j + 1];
+    preact<W, 2>(v, w, bias, x, U - 1);
+    if (SILU) silu<2>(v);
+    st_vec<E, 4>(static_cast<E*>(a.y) + (size_t)row * a.ldy + c, v);
 }
 
 // ---------------------------------------------------------------- dispatch
@@ -522,74 +638,86 @@ cudaError_t dispatch(int width, bool silu, int io_bf16, F f) {
 
 }  // namespace
 
-// Rows a piece: enough pieces for about 1536 threads per SM, at least 8 rows (the W-1 rows before a
-// piece are read twice) and at most 64.
-int rows_per_piece(int64_t rows, int64_t D, int lo, int hi) {
-    const int64_t g = rows * ((D + 31) / 32 * 8) / (148 * 1536);
-    return (int)(g < lo ? lo : (g > hi ? hi : g));
+// Rows a piece of one batch entry: as many as give one wave of CTAs, at least 8 (the W-1 rows before a
+// piece are read twice) and at most 512 (the gradient adds a piece's rows one after another in fp32;
+// its sums over pieces are pairwise or short).  A multiple of four: a word of step exponents.
+int rows_per_piece(int64_t batch, int64_t rows, const Tile& t) {
+    const int64_t tiles = (int64_t)t.nct * (batch > 0 ? batch : 1), room = (int64_t)kResident * t.ry;
+    int64_t n = room / tiles;
+    if (n < 4) n = 4 * room / tiles;  // too few per entry to fill a wave evenly: shorter pieces, more waves
+    if (n < 1) n = 1;
+    int64_t g = ((rows + n - 1) / n + 3) / 4 * 4;
+    return (int)(g < 8 ? 8 : (g > 512 ? 512 : g));
 }
+
+template <typename K, typename A>
+cudaError_t launch(K kern, dim3 grid, int smem, const A& a, cudaStream_t st) {
+    if (smem >= 48 * 1024) {  // the prompts' kernel has static shared memory besides
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    kern<<<grid, kThreads, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+// Channels a thread of the forward and the prompts: 16 bytes of x.
+template <typename E> constexpr int kV = 16 / (int)sizeof(E);
 
 }  // namespace conv
 
-static void set_pieces(ConvArgs& a, int lo, int hi) {
-    const conv::Tile t = conv::tile_of(a.D);
+void conv_plan(ConvArgs& a, int io_bf16, bool backward) {
+    const conv::Tile t = conv::tile_of(a.D, backward || !io_bf16 ? 4 : 8);
     a.cx = t.cx; a.ry = t.ry; a.nct = t.nct;
-    const int G = conv::rows_per_piece((int64_t)a.B * a.L, a.D, lo, hi);
-    a.nseg = a.L > 0 ? (a.L + G - 1) / G : 1;
-    a.G = a.L > 0 ? (a.L + a.nseg - 1) / a.nseg : 1;
+    a.G = conv::rows_per_piece(a.B, a.L, t);
     a.nseg = a.L > 0 ? (a.L + a.G - 1) / a.G : 1;
     a.parts = (int)(((int64_t)a.B * a.nseg + t.ry - 1) / t.ry);
-}
-void conv_plan(ConvArgs& a, bool backward) {
-    if (backward) set_pieces(a, 16, 64);
-    else set_pieces(a, 8, 64);
+    a.Lq = ((size_t)a.L + 3) / 4 * 4;
 }
 
 cudaError_t launch_conv_fwd(const ConvArgs& a, int width, bool silu, int io_bf16, bool restore,
                             cudaStream_t st) {
-    const dim3 grid(a.parts, a.nct), block(a.cx * a.ry);
-    return conv::dispatch(width, silu, io_bf16, [&](auto e, auto w, auto s) {
+    using namespace conv;
+    const dim3 grid(a.parts, a.nct);
+    return dispatch(width, silu, io_bf16, [&](auto e, auto w, auto s) {
         using E = typename decltype(e)::type;
-        constexpr int W = decltype(w)::value;
+        constexpr int W = decltype(w)::value, V = kV<E>;
         constexpr bool SL = decltype(s)::value != 0;
         if (restore)
-            conv::conv_fwd_kernel<E, W, SL, true, false><<<grid, block, 0, st>>>(a);
-        else if (a.q_out)
-            conv::conv_fwd_kernel<E, W, SL, false, true><<<grid, block, 0, st>>>(a);
-        else
-            conv::conv_fwd_kernel<E, W, SL, false, false><<<grid, block, 0, st>>>(a);
-        return cudaGetLastError();
+            return launch(conv_fwd_kernel<E, V, W, SL, true, false>, grid, Fwd<E, V, W, SL, true, false>::kBytes, a, st);
+        if (a.q_out)
+            return launch(conv_fwd_kernel<E, V, W, SL, false, true>, grid, Fwd<E, V, W, SL, false, true>::kBytes, a, st);
+        return launch(conv_fwd_kernel<E, V, W, SL, false, false>, grid, Fwd<E, V, W, SL, false, false>::kBytes, a, st);
     });
 }
 
 cudaError_t launch_conv_bwd(const ConvArgs& a, int width, bool silu, int io_bf16, cudaStream_t st) {
-    const dim3 grid(a.parts, a.nct), block(a.cx * a.ry);
-    cudaError_t e0 = conv::dispatch(width, silu, io_bf16, [&](auto e, auto w, auto s) {
+    using namespace conv;
+    const dim3 grid(a.parts, a.nct);
+    const cudaError_t e0 = dispatch(width, silu, io_bf16, [&](auto e, auto w, auto s) {
         using E = typename decltype(e)::type;
         constexpr int W = decltype(w)::value;
         constexpr bool SL = decltype(s)::value != 0;
-        if (a.q)
-            conv::conv_bwd_kernel<E, W, SL, true><<<grid, block, 0, st>>>(a);
-        else
-            conv::conv_bwd_kernel<E, W, SL, false><<<grid, block, 0, st>>>(a);
-        return cudaGetLastError();
+        if (a.q) return launch(conv_bwd_kernel<E, W, SL, true>, grid, Bwd<E, true>::kBytes, a, st);
+        return launch(conv_bwd_kernel<E, W, SL, false>, grid, Bwd<E, false>::kBytes, a, st);
     });
     if (e0 != cudaSuccess) return e0;
-    conv::conv_reduce_kernel<<<dim3((a.D + 31) / 32, width + 1), 256, 0, st>>>(a.part, a.parts, a.D, width,
-                                                                              a.dw, a.dbias);
+    conv_reduce_kernel<<<dim3((a.D + 31) / 32, width + 1), 256, 0, st>>>(a.part, a.parts, a.D, width, a.dw,
+                                                                        a.dbias, a.status);
     return cudaGetLastError();
 }
 
 cudaError_t launch_conv_prompt(ConvServeArgs a, int width, bool silu, int io_bf16, cudaStream_t st) {
-    const conv::Tile t = conv::tile_of(a.D);
+    using namespace conv;
+    const Tile t = tile_of(a.D, io_bf16 ? 8 : 4);
     a.cx = t.cx; a.ry = t.ry;
-    a.G = conv::rows_per_piece(a.rows, a.D, 8, 64);
+    a.G = rows_per_piece(1, a.rows, t);
     a.items = (int64_t)(a.rows / a.G) + a.S;
-    const dim3 grid((unsigned)((a.items + t.ry - 1) / t.ry), t.nct), block(256);  // whole warps
-    return conv::dispatch(width, silu, io_bf16, [&](auto e, auto w, auto s) {
+    const dim3 grid((unsigned)((a.items + t.ry - 1) / t.ry), t.nct);
+    return dispatch(width, silu, io_bf16, [&](auto e, auto w, auto s) {
         using E = typename decltype(e)::type;
-        conv::conv_prompt_kernel<E, decltype(w)::value, decltype(s)::value != 0><<<grid, block, 0, st>>>(a);
-        return cudaGetLastError();
+        constexpr int W = decltype(w)::value, V = kV<E>;
+        constexpr bool SL = decltype(s)::value != 0;
+        return launch(conv_prompt_kernel<E, V, W, SL>, grid, Fwd<E, V, W, SL, false, false>::kBytes, a, st);
     });
 }
 

@@ -15,11 +15,17 @@ __device__ __forceinline__ void flag_if(unsigned* status, unsigned code) {
     if (status) flag_status(status, code);
 }
 
-// ---------------------------------------------------------------- four consecutive channels
-// Raw loads (16 bytes of fp32, 8 of bf16) are kept apart from the conversion so that several can
-// be in flight.
-template <typename E> struct Quad;
-template <> struct Quad<float> {
+// ---------------------------------------------------------------- V consecutive channels
+// Raw vectors (as loaded) are kept apart from the conversion to V / 2 fp32 pairs.
+__device__ __forceinline__ float2 bf16_pair(unsigned r) {
+    return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+}
+__device__ __forceinline__ unsigned pack_bf16(float2 v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const unsigned*>(&a);
+}
+template <typename E, int V> struct Vec;
+template <> struct Vec<float, 4> {
     using Raw = float4;
     static __device__ __forceinline__ Raw zero() { return make_float4(0.f, 0.f, 0.f, 0.f); }
     static __device__ __forceinline__ void unpack(const Raw& r, float2 (&o)[2]) {
@@ -30,26 +36,61 @@ template <> struct Quad<float> {
         return make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
     }
 };
-template <> struct Quad<__nv_bfloat16> {
+template <> struct Vec<__nv_bfloat16, 4> {
     using Raw = uint2;
     static __device__ __forceinline__ Raw zero() { return make_uint2(0u, 0u); }
     static __device__ __forceinline__ void unpack(const Raw& r, float2 (&o)[2]) {
-        o[0] = make_float2(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u));
-        o[1] = make_float2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
+        o[0] = bf16_pair(r.x);
+        o[1] = bf16_pair(r.y);
     }
     static __device__ __forceinline__ Raw pack(const float2 (&v)[2]) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0].x, v[0].y);
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[1].x, v[1].y);
-        return make_uint2(*reinterpret_cast<const unsigned*>(&a), *reinterpret_cast<const unsigned*>(&b));
+        return make_uint2(pack_bf16(v[0]), pack_bf16(v[1]));
     }
 };
-template <typename E>
-__device__ __forceinline__ typename Quad<E>::Raw ld_quad(const E* p) {
-    return *reinterpret_cast<const typename Quad<E>::Raw*>(p);
+template <> struct Vec<__nv_bfloat16, 8> {
+    using Raw = uint4;
+    static __device__ __forceinline__ Raw zero() { return make_uint4(0u, 0u, 0u, 0u); }
+    static __device__ __forceinline__ void unpack(const Raw& r, float2 (&o)[4]) {
+        o[0] = bf16_pair(r.x);
+        o[1] = bf16_pair(r.y);
+        o[2] = bf16_pair(r.z);
+        o[3] = bf16_pair(r.w);
+    }
+    static __device__ __forceinline__ Raw pack(const float2 (&v)[4]) {
+        return make_uint4(pack_bf16(v[0]), pack_bf16(v[1]), pack_bf16(v[2]), pack_bf16(v[3]));
+    }
+};
+template <typename E, int V>
+__device__ __forceinline__ typename Vec<E, V>::Raw ld_vec(const E* p) {
+    return *reinterpret_cast<const typename Vec<E, V>::Raw*>(p);
 }
-template <typename E>
-__device__ __forceinline__ void st_quad(E* p, const float2 (&v)[2]) {
-    *reinterpret_cast<typename Quad<E>::Raw*>(p) = Quad<E>::pack(v);
+template <typename E, int V>
+__device__ __forceinline__ void st_vec(E* p, const float2 (&v)[V / 2]) {
+    *reinterpret_cast<typename Vec<E, V>::Raw*>(p) = Vec<E, V>::pack(v);
+}
+
+// sigmoid s of a pair, and 1 - s = e s with e = exp(-v), with three special-function operations
+// instead of four: the two quotients share one reciprocal, 1/a = b (1/ab).  v is first held above
+// -43.6 (where v s is -5e-18), so that the product ab stays below 2^126; max.NaN keeps a NaN in
+// v, while fminf keeps it out of e, from where it would reach the neighbour.
+__device__ __forceinline__ float hold(float v) {
+    float o;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(v), "f"(-43.6f));
+    return o;
+}
+__device__ __forceinline__ void sigmoid_pair(float2& v, float2& s, float2& e) {
+    v = make_float2(hold(v.x), hold(v.y));
+    const float2 z = __fmul2_rn(v, make_float2(-kLog2e, -kLog2e));
+    e = make_float2(ex2_mufu(fminf(z.x, 63.f)), ex2_mufu(fminf(z.y, 63.f)));
+    const float2 a = __fadd2_rn(e, make_float2(1.f, 1.f));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a.x * a.y));
+    s = __fmul2_rn(make_float2(r, r), make_float2(a.y, a.x));
+}
+__device__ __forceinline__ float2 silu_pair(float2 v) {
+    float2 s, e;
+    sigmoid_pair(v, s, e);
+    return __fmul2_rn(v, s);
 }
 
 // v sigmoid(v).  exp(-v) overflows to infinity below -88, where the quotient is zero, as v sigmoid(v)

@@ -40,9 +40,9 @@ constexpr int kThreads = 128;
 
 // four B or C elements of a row, as fp32
 template <typename E>
-__device__ __forceinline__ float4 quad_f4(const typename Quad<E>::Raw& r) {
+__device__ __forceinline__ float4 quad_f4(const typename Vec<E, 4>::Raw& r) {
     float2 o[2];
-    Quad<E>::unpack(r, o);
+    Vec<E, 4>::unpack(r, o);
     return make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
 }
 
@@ -119,14 +119,14 @@ __global__ void __launch_bounds__(kThreads) scan_prompt_kernel(ScanServeArgs a) 
 
     // B and C of steps [t, t + 32): zero past the segment's end, so that a step which is not there
     // (delta = 0: transition one) adds nothing to the state
-    typename Quad<E>::Raw rB[PER], rC[PER];
+    typename Vec<E, 4>::Raw rB[PER], rC[PER];
     auto fetch = [&](int t) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int q = tid + i * kThreads, row = q / (N / 4), col = (q % (N / 4)) * 4;
             const bool ok = q < NQ && t + row < n;
-            rB[i] = ok ? ld_quad(pB + (size_t)(t + row) * a.ldb + col) : Quad<E>::zero();
-            if (!SUMMARY) rC[i] = ok ? ld_quad(pC + (size_t)(t + row) * a.ldc + col) : Quad<E>::zero();
+            rB[i] = ok ? ld_vec<E, 4>(pB + (size_t)(t + row) * a.ldb + col) : Vec<E, 4>::zero();
+            if (!SUMMARY) rC[i] = ok ? ld_vec<E, 4>(pC + (size_t)(t + row) * a.ldc + col) : Vec<E, 4>::zero();
         }
     };
     auto stage = [&](int k) {
@@ -271,14 +271,14 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanServeArgs a) {
         h4[r] = work ? *reinterpret_cast<const float4*>(a.pool + ((size_t)k[r] * a.D + d) * N + n0)
                      : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    typename Quad<E>::Raw rB[R], rC[R];
+    typename Vec<E, 4>::Raw rB[R], rC[R];
     E x[R], dr[R], z[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const bool work = dv && k[r] >= 0 && k[r] < a.slots;
         const size_t row = work ? row0 + r : 0;
-        rB[r] = work ? ld_quad(static_cast<const E*>(a.Bm) + row * a.ldb + n0) : Quad<E>::zero();
-        rC[r] = work ? ld_quad(static_cast<const E*>(a.Cm) + row * a.ldc + n0) : Quad<E>::zero();
+        rB[r] = work ? ld_vec<E, 4>(static_cast<const E*>(a.Bm) + row * a.ldb + n0) : Vec<E, 4>::zero();
+        rC[r] = work ? ld_vec<E, 4>(static_cast<const E*>(a.Cm) + row * a.ldc + n0) : Vec<E, 4>::zero();
         x[r] = work ? static_cast<const E*>(a.x)[row * a.ldx + d] : Elem<E>::from_f(0.f);
         dr[r] = work ? static_cast<const E*>(a.draw)[row * a.ldd + d] : Elem<E>::from_f(0.f);
         z[r] = work && a.z ? static_cast<const E*>(a.z)[row * a.ldz + d] : Elem<E>::from_f(0.f);
@@ -310,8 +310,8 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanServeArgs a) {
         const float dlt = softplus_fast(Elem<E>::to_f(dr[r]));
         const float2 dd = make_float2(dlt, dlt * xf);
         float2 bq[2], cq[2], acc = f2(0.f);
-        Quad<E>::unpack(rB[r], bq);
-        Quad<E>::unpack(rC[r], cq);
+        Vec<E, 4>::unpack(rB[r], bq);
+        Vec<E, 4>::unpack(rC[r], cq);
         float2 h[2] = {make_float2(h4[r].x, h4[r].y), make_float2(h4[r].z, h4[r].w)};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

@@ -164,10 +164,11 @@ cudaError_t launch_dtproj_fwd(const DtArgs& a, cudaStream_t st);
 cudaError_t launch_dtproj_bwd(const DtArgs& a, cudaStream_t st);
 
 // Short causal convolution (csrc/conv.cu).  A piece is G rows of one batch entry; a CTA takes ry
-// pieces of cx four-channel vectors; parts CTAs cover the nseg * B pieces, nct the channels.
+// pieces of cx vectors of channels; parts CTAs cover the nseg * B pieces, nct the channels.
 struct ConvArgs {
     int B, L, D, G, nseg, parts, cx, ry, nct;
     size_t ldx, ldy, lddy, lddx;
+    size_t Lq;            // bytes of one group's step exponents: L rounded up to four
     const void* x;
     const int8_t* q;      // 8-bit checkpoint in (restore, backward)
     const uint8_t* qe;
@@ -185,8 +186,9 @@ struct ConvArgs {
     float* part;          // [parts][W+1][D] sums of dw and dbias
     float* dw;
     float* dbias;
+    unsigned* status;     // backward
 };
-void conv_plan(ConvArgs& a, bool backward);  // fills G, nseg, parts, cx, ry, nct from B, L, D
+void conv_plan(ConvArgs& a, int io_bf16, bool backward);  // fills G, nseg, parts, cx, ry, nct, Lq
 cudaError_t launch_conv_fwd(const ConvArgs& a, int width, bool silu, int io_bf16, bool restore,
                             cudaStream_t st);
 cudaError_t launch_conv_bwd(const ConvArgs& a, int width, bool silu, int io_bf16, cudaStream_t st);

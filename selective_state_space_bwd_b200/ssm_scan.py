@@ -689,8 +689,12 @@ def conv_shape(batch, seqlen, dim, width, io=SSM_BF16, silu=True, ldx=0, ldy=0, 
 def _q8_expect(q8, shape, device):
     q, qe = q8
     _expect(q, "q", shape, torch.int8, device)
-    _expect(qe, "qe", (*shape[:-1], -(-shape[-1] // 32)), torch.uint8, device)
+    _expect(qe, "qe", _qe_shape(*shape), torch.uint8, device)
     return q, qe
+
+
+def _qe_shape(B, L, D):
+    return B, -(-D // 32), -(-L // 4) * 4
 
 
 def ssm_conv_fwd(x, w, bias=None, silu=True, s0=None, want_sL=False, want_q8=False, y=None, sL=None,
@@ -698,7 +702,7 @@ def ssm_conv_fwd(x, w, bias=None, silu=True, s0=None, want_sL=False, want_q8=Fal
     """Short causal convolution y = [SiLU](bias + sum_j w[:, j] x_{t-(W-1)+j}).  x [B,L,D] fp32 or
     bf16, rows may be strided; w [D,W] (W = 2..4), bias [D] fp32; s0 [B,W-1,D] the inputs before
     step 0 (None: zero).  Returns (y [B,L,D], sL, q8): sL [B,W-1,D] the last inputs (if ``want_sL`` or
-    ``sL`` is given, else None), q8 = (q [B,L,D] int8, qe [B,L,ceil(D/32)] uint8) the 8-bit
+    ``sL`` is given, else None), q8 = (q [B,L,D] int8, qe [B, ceil(D/32), L rounded up to 4] uint8) the 8-bit
     checkpoint of x (if ``want_q8`` or ``q8`` is given, else None)."""
     dev, io = _io_tensor(x, "x", 3)
     B, L, D = x.shape
@@ -712,7 +716,7 @@ def ssm_conv_fwd(x, w, bias=None, silu=True, s0=None, want_sL=False, want_q8=Fal
             sL = torch.empty((B, W - 1, D), dtype=x.dtype, device=dev)
         if q8 is None and want_q8:
             q8 = (torch.empty((B, L, D), dtype=torch.int8, device=dev),
-                  torch.empty((B, L, -(-D // 32)), dtype=torch.uint8, device=dev))
+                  torch.empty(_qe_shape(B, L, D), dtype=torch.uint8, device=dev))
         ldy = _expect_rows(y, "y", x.shape, x.dtype, dev)
         _expect(sL, "sL", (B, W - 1, D), x.dtype, dev)
         q, qe = _q8_expect(q8, x.shape, dev) if q8 is not None else (None, None)

@@ -96,22 +96,41 @@ constexpr unsigned kTopStep = 248u;
 
 // The biased exponent of a group's step from the largest magnitude's bits (an unsigned maximum, so
 // that a NaN, above every number's bits, is not lost as fmaxf would lose it).
+// 127.5 / 64 has the mantissa 0x7f0000, so that adding 2^16 carries into the exponent from there on.
 __device__ __forceinline__ unsigned step_exponent(unsigned top) {
-    if (top == 0u) return 0u;
-    const unsigned e = top >> 23;
-    if (e == 255u) return 255u;
-    unsigned q = e > 7u ? e - 6u : 1u;
-    // 2^-(step): q is at most kTopStep, so the factor is a normal number
-    if (q < kTopStep && __uint_as_float(top) * __uint_as_float((254u - q) << 23) >= 127.5f) ++q;
+    unsigned q = min(max((top + 0x10000u) >> 23, 7u) - 6u, kTopStep);
+    if (top == 0u) q = 0u;
+    if (top >= 0x7f800000u) q = 255u;
     return q;
+}
+
+// The largest magnitude of V channels, as fp32 bits; bf16 pairs are compared as they lie in the row.
+template <typename E, int P>
+__device__ __forceinline__ unsigned top_of(const float2 (&x)[P]) {
+    unsigned m[P];
+    if constexpr (sizeof(E) == 2) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            m[p] = __byte_perm(__float_as_uint(x[p].x), __float_as_uint(x[p].y), 0x7632) & 0x7fff7fffu;
+#pragma unroll
+        for (int p = 1; p < P; ++p) m[0] = __vmaxu2(m[0], m[p]);
+        return max(m[0] << 16, m[0] & 0xffff0000u);
+    } else {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            m[p] = max(__float_as_uint(x[p].x) & 0x7fffffffu, __float_as_uint(x[p].y) & 0x7fffffffu);
+#pragma unroll
+        for (int p = 1; p < P; ++p) m[0] = max(m[0], m[p]);
+        return m[0];
+    }
 }
 
 // Four int8 of x / 2^(qe - 127), rounded to nearest even: adding 1.5 * 2^23 leaves the rounded
 // integer in the low bits of the sum (the product by a power of two is exact).
 __device__ __forceinline__ unsigned quantise4(float2 x0, float2 x1, unsigned qe) {
-    if (qe == 0u || qe == 255u) return 0u;
-    const float f = __uint_as_float((254u - qe) << 23);
-    if (qe == kTopStep) {
+    const float f = __uint_as_float((254u - qe) << 23);  // a normal number; zeros (qe 0) stay zeros
+    if (qe >= kTopStep) {
+        if (qe == 255u) return 0u;
         const float m = 127.0f * __uint_as_float(kTopStep << 23);
         x0 = make_float2(fminf(fmaxf(x0.x, -m), m), fminf(fmaxf(x0.y, -m), m));
         x1 = make_float2(fminf(fmaxf(x1.x, -m), m), fminf(fmaxf(x1.y, -m), m));
@@ -272,13 +291,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(ConvArgs a) {
             if (cv) st_vec<E, V>(y, v);
             y += a.ldy;
             if (DST8) {
-                unsigned top = 0u;
-                if (cv) {
-#pragma unroll
-                    for (int p = 0; p < P; ++p)
-                        top = max(top, max(__float_as_uint(x[u][p].x) & 0x7fffffffu,
-                                           __float_as_uint(x[u][p].y) & 0x7fffffffu));
-                }
+                unsigned top = cv ? top_of<E, P>(x[u]) : 0u;
                 constexpr int GL = 32 / V;  // lanes of a group
                 const unsigned grp = ((1u << GL) - 1u) << (threadIdx.x & (32 - GL));
 #pragma unroll
@@ -642,9 +655,10 @@ cudaError_t dispatch(int width, bool silu, int io_bf16, F f) {
 // piece are read twice) and at most 512 (the gradient adds a piece's rows one after another in fp32;
 // its sums over pieces are pairwise or short).  A multiple of four: a word of step exponents.
 int rows_per_piece(int64_t batch, int64_t rows, const Tile& t) {
-    const int64_t tiles = (int64_t)t.nct * (batch > 0 ? batch : 1), room = (int64_t)kResident * t.ry;
-    int64_t n = room / tiles;
-    if (n < 4) n = 4 * room / tiles;  // too few per entry to fill a wave evenly: shorter pieces, more waves
+    if (batch < 1) batch = 1;
+    const int64_t room = (int64_t)(kResident / t.nct) * t.ry;  // pieces of one channel tile in a wave
+    int64_t n = room / batch;
+    if (n < 4) n = 4 * room / batch;  // too few per entry to fill a wave evenly: shorter pieces, more waves
     if (n < 1) n = 1;
     int64_t g = ((rows + n - 1) / n + 3) / 4 * 4;
     return (int)(g < 8 ? 8 : (g > 512 ? 512 : g));

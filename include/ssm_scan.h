@@ -424,9 +424,9 @@ typedef struct ssm_conv_shape {
     int64_t batch;   /* B >= 0, at most 65535 */
     int64_t seqlen;  /* L >= 0, at most 2^30 */
     int64_t dim;     /* D >= 1, at most 2^22; D * sizeof(io) a multiple of 16 bytes */
-    int64_t ldx;     /* row strides of x, y, dy, dx in elements: 0 = D, else at least D and a */
-    int64_t ldy;     /*   multiple of 16 bytes; only those of the call's own arrays are used,  */
-    int64_t lddy;    /*   all are checked                                                      */
+    int64_t ldx;     /* row strides of x, y, dy, dx in elements: 0 = D, else D..2^29 and a    */
+    int64_t ldy;     /*   multiple of 16 bytes; only those of the call's own arrays are used, */
+    int64_t lddy;    /*   all are checked                                                     */
     int64_t lddx;
     int32_t width;   /* W, one of 2, 3, 4 */
     int32_t io;      /* ssm_dtype */
@@ -485,7 +485,7 @@ int ssm_conv_bwd(const ssm_conv_shape* shape, const void* x, const int8_t* q, co
  * other scans.  ws may be NULL (ws_bytes 0) where a call needs only the status word (256 bytes): then
  * nothing is recorded, and the call is one kernel with no memset before it.
  *
- * Row strides in elements, 0 = dense; at least the row's length; of x, y, delta_raw and z a multiple
+ * Row strides in elements, 0 = dense; from the row's length to 2^29; of x, y, delta_raw and z a multiple
  * of 16 bytes with 16-byte aligned pointers, of Bm and Cm a multiple of 4 elements with pointers aligned
  * to 4 elements: columns of a projection's output are used in place.  offsets and slot are
  * aligned to 4 bytes.  Outputs must not overlap inputs.

@@ -14,11 +14,12 @@ namespace {
 
 int check_io(int32_t io) { return io == SSM_F32 || io == SSM_BF16 ? SSM_OK : SSM_ERR_UNSUPPORTED; }
 
-// A row stride (0 = the row's length): at least the row, a multiple of `unit` elements, and small enough
-// that stride * rows stays within 2^62.
+// A row stride (0 = the row's length): at least the row, a multiple of `unit` elements, and below 2^29, so
+// that its bytes fit 32 bits.
 int check_ld(int64_t ld, int64_t len, int64_t unit) {
     if (ld == 0) return SSM_OK;
-    if (ld < len || ld > (int64_t)1 << 31) return SSM_ERR_INVALID_ARG;
+    if (ld < len) return SSM_ERR_INVALID_ARG;
+    if (ld > (int64_t)1 << 29) return SSM_ERR_UNSUPPORTED;
     return ld % unit == 0 ? SSM_OK : SSM_ERR_MISALIGNED;
 }
 size_t stride(int64_t ld, int64_t len) { return (size_t)(ld ? ld : len); }

@@ -1,8 +1,8 @@
 // Short causal convolution in front of the scan: forward, its recomputation from an 8-bit
 // checkpoint, its gradient, and the packed-prompt and single-token forms (include/ssm_scan.h).
 //
-// Every kernel is bound by memory traffic, with the special-function unit (three operations for
-// two SiLUs) and, in the gradient, the fp32 pipes not far behind.  A thread owns V consecutive
+// Every kernel is bound by memory traffic, with the instructions (SiLU, conversion, W products) and,
+// in the gradient, the fp32 pipes not far behind.  A thread owns V consecutive
 // channels and walks down a piece of the rows, the last W-1 inputs in registers, so that an element
 // is read once from DRAM (the W-1 rows before a piece a second time).  Each thread copies its
 // own rows into its own places of a ring in shared memory, kDepth groups of four rows ahead
@@ -165,10 +165,10 @@ template <typename E, int V, bool Q8> struct Rows;
 template <typename E, int V> struct Rows<E, V, false> {
     using Raw = typename Vec<E, V>::Raw;
     const E* x;
-    size_t ld;
+    unsigned ldb;
     __device__ __forceinline__ Rows(const ConvArgs& a, int b, int c)
-        : x(static_cast<const E*>(a.x) + (size_t)b * a.L * a.ldx + c), ld(a.ldx) {}
-    __device__ __forceinline__ const void* at(int t) const { return x + (size_t)t * ld; }
+        : x(static_cast<const E*>(a.x) + (size_t)b * a.L * a.ldx + c), ldb((unsigned)(a.ldx * sizeof(E))) {}
+    __device__ __forceinline__ const void* at(int t) const { return row_at(x, t, ldb); }
     __device__ __forceinline__ unsigned word(int) const { return 0u; }
     static __device__ __forceinline__ void unpack(const Raw& r, unsigned, float2 (&o)[V / 2]) {
         Vec<E, V>::unpack(r, o);
@@ -181,11 +181,11 @@ template <typename E> struct Rows<E, 4, true> {
     using Raw = unsigned;
     const int8_t* q;
     const uint8_t* e;
-    size_t D;
+    unsigned D;
     __device__ __forceinline__ Rows(const ConvArgs& a, int b, int c)
         : q(a.q + (size_t)b * a.L * a.D + c),
-          e(a.qe + ((size_t)b * ((a.D + 31) / 32) + c / 32) * a.Lq), D(a.D) {}
-    __device__ __forceinline__ const void* at(int t) const { return q + (size_t)t * D; }
+          e(a.qe + ((size_t)b * ((a.D + 31) / 32) + c / 32) * a.Lq), D((unsigned)a.D) {}
+    __device__ __forceinline__ const void* at(int t) const { return row_at(q, t, D); }
     __device__ __forceinline__ unsigned word(int t) const { return *reinterpret_cast<const unsigned*>(e + t); }
     static __device__ __forceinline__ void unpack(const Raw& r, unsigned e, float2 (&o)[2]) {
         restore4(o[0], o[1], r, e);
@@ -198,11 +198,11 @@ template <typename E> struct Rows<E, 8, true> {
     using Raw = uint2;
     const int8_t* q;
     const uint8_t* e;
-    size_t D;
+    unsigned D;
     __device__ __forceinline__ Rows(const ConvArgs& a, int b, int c)
         : q(a.q + (size_t)b * a.L * a.D + c),
-          e(a.qe + ((size_t)b * ((a.D + 31) / 32) + c / 32) * a.Lq), D(a.D) {}
-    __device__ __forceinline__ const void* at(int t) const { return q + (size_t)t * D; }
+          e(a.qe + ((size_t)b * ((a.D + 31) / 32) + c / 32) * a.Lq), D((unsigned)a.D) {}
+    __device__ __forceinline__ const void* at(int t) const { return row_at(q, t, D); }
     __device__ __forceinline__ unsigned word(int t) const { return *reinterpret_cast<const unsigned*>(e + t); }
     static __device__ __forceinline__ void unpack(const Raw& r, unsigned e, float2 (&o)[4]) {
         restore4(o[0], o[1], r.x, e);
@@ -272,8 +272,9 @@ __global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(ConvArgs a) {
         else
             rows.load(t0 - j, x[U - j]);
     }
-    E* y = static_cast<E*>(a.y) + ((size_t)b * a.L + t0) * a.ldy + cc;
-    size_t qo = DST8 ? ((size_t)b * a.L + t0) * a.D + cc : 0;
+    E* y = static_cast<E*>(a.y) + (size_t)b * a.L * a.ldy + cc;
+    const unsigned ldyb = (unsigned)(a.ldy * sizeof(E));
+    int8_t* qo = DST8 ? a.q_out + (size_t)b * a.L * a.D + cc : nullptr;
     int stage = 0;
     for (int t = t0; t < t1; t += U) {
         issue(t + (DEPTH - 1) * U, stage == 0 ? DEPTH - 1 : stage - 1);
@@ -288,8 +289,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(ConvArgs a) {
             float2 v[P];
             preact<W, P>(v, w, bias, x, u);
             if (SILU) silu<P>(v);
-            if (cv) st_vec<E, V>(y, v);
-            y += a.ldy;
+            if (cv) st_vec<E, V>(row_at(y, t + u, ldyb), v);
             if (DST8) {
                 unsigned top = cv ? top_of<E, P>(x[u]) : 0u;
                 constexpr int GL = 32 / V;  // lanes of a group
@@ -300,12 +300,11 @@ __global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(ConvArgs a) {
                 steps |= e << (8 * u);
                 if (cv) {
                     if constexpr (V == 4)
-                        *reinterpret_cast<unsigned*>(a.q_out + qo) = quantise4(x[u][0], x[u][1], e);
+                        *reinterpret_cast<unsigned*>(row_at(qo, t + u, a.D)) = quantise4(x[u][0], x[u][1], e);
                     else
-                        *reinterpret_cast<uint2*>(a.q_out + qo) =
+                        *reinterpret_cast<uint2*>(row_at(qo, t + u, a.D)) =
                             make_uint2(quantise4(x[u][0], x[u][1], e), quantise4(x[u][P - 2], x[u][P - 1], e));
                 }
-                qo += a.D;
             }
         }
         if (DST8 && cv && (c & 31) == 0)
@@ -368,11 +367,12 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
         const int lo = t0 > 0 ? t0 : -(W - 1);  // rows whose gradient this piece writes: lo..t1-1
         const R rows(a, b, c);
         const E* dy = static_cast<const E*>(a.dy) + (size_t)b * a.L * a.lddy + c;
+        const unsigned lddyb = (unsigned)(a.lddy * sizeof(E)), lddxb = (unsigned)(a.lddx * sizeof(E));
         auto issue = [&](int t, int stage) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (t + u < tend) {
-                    cp_async<sizeof(GRaw)>(gring + (stage * U + u) * kThreads, dy + (size_t)(t + u) * a.lddy);
+                    cp_async<sizeof(GRaw)>(gring + (stage * U + u) * kThreads, row_at(dy, t + u, lddyb));
                     cp_async<sizeof(Raw)>(xring + (stage * U + u) * kThreads, rows.at(t + u));
                 }
             cp_async_commit();
@@ -406,11 +406,11 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
                 preact<W, 2>(v, w, bias, x, u);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    // d (v s) / dv = s (1 + v (1 - s)), with 1 - s = e s exact where s is next to 1
-                    float2 s, e;
-                    sigmoid_pair(v[p], s, e);
-                    g[u][p] = __fmul2_rn(g[u][p], __fmul2_rn(s, __ffma2_rn(v[p], __fmul2_rn(e, s),
-                                                                            make_float2(1.f, 1.f))));
+                    // d (v s) / dv = s (1 + v (1 - s))
+                    const float2 one = make_float2(1.f, 1.f);
+                    const float2 s = sigmoid_pair(v[p]);
+                    const float2 r = __ffma2_rn(s, make_float2(-1.f, -1.f), one);
+                    g[u][p] = __fmul2_rn(g[u][p], __fmul2_rn(s, __ffma2_rn(v[p], r, one)));
                 }
             }
             if (!INNER && t >= tend) g[u][0] = g[u][1] = make_float2(0.f, 0.f);  // the ring holds other rows
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
                 d[1] = __fadd2_rn(d[1], e[1]);
             }
             if (INNER || r >= 0)
-                st_vec<E, 4>(dx + (size_t)r * a.lddx, d);
+                st_vec<E, 4>(row_at(dx, r, lddxb), d);
             else if (ds0)
                 st_vec<E, 4>(ds0 + (size_t)(r + W - 1) * a.D, d);
         };
@@ -538,10 +538,11 @@ __global__ void __launch_bounds__(kThreads, 2) conv_prompt_kernel(ConvServeArgs 
     if (c >= a.D) return;
     const int t0 = sp.first, t1 = min(sp.end, t0 + a.G);
     const E* xr = static_cast<const E*>(a.x) + c;
+    const unsigned ldxb = (unsigned)(a.ldx * sizeof(E)), ldyb = (unsigned)(a.ldy * sizeof(E));
     auto issue = [&](int t, int stage) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (t + u < t1) cp_async<sizeof(Raw)>(ring + (stage * U + u) * kThreads, xr + (size_t)(t + u) * a.ldx);
+            if (t + u < t1) cp_async<sizeof(Raw)>(ring + (stage * U + u) * kThreads, row_at(xr, t + u, ldxb));
         cp_async_commit();
     };
 #pragma unroll
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_prompt_kernel(ConvServeArgs 
 #pragma unroll
         for (int j = 1; j < W; ++j) Vec<E, V>::unpack(ld_vec<E, V>(xr + (size_t)(t0 - j) * a.ldx), x[U - j]);
     }
-    E* y = static_cast<E*>(a.y) + (size_t)t0 * a.ldy + c;
+    E* y = static_cast<E*>(a.y) + c;
     int stage = 0;
     for (int t = t0; t < t1; t += U) {
         issue(t + (DEPTH - 1) * U, stage == 0 ? DEPTH - 1 : stage - 1);
@@ -592,8 +593,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_prompt_kernel(ConvServeArgs 
             float2 v[P];
             preact<W, P>(v, w, bias, x, u);
             if (SILU) silu<P>(v);
-            st_vec<E, V>(y, v);
-            y += a.ldy;
+            st_vec<E, V>(row_at(y, t + u, ldyb), v);
         }
         stage = stage == DEPTH - 1 ? 0 : stage + 1;
     }

@@ -69,34 +69,28 @@ __device__ __forceinline__ void st_vec(E* p, const float2 (&v)[V / 2]) {
     *reinterpret_cast<typename Vec<E, V>::Raw*>(p) = Vec<E, V>::pack(v);
 }
 
-// sigmoid s of a pair, and 1 - s = e s with e = exp(-v), with three special-function operations
-// instead of four: the two quotients share one reciprocal, 1/a = b (1/ab).  v is first held above
-// -43.6 (where v s is -5e-18), so that the product ab stays below 2^126; max.NaN keeps a NaN in
-// v, while fminf keeps it out of e, from where it would reach the neighbour.
-__device__ __forceinline__ float hold(float v) {
-    float o;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(v), "f"(-43.6f));
-    return o;
+// sigmoid(v) from the exp2 and reciprocal units.  exp(-v) overflows to infinity below -88, where the
+// quotient is zero, as sigmoid is to fp32's normal numbers.  (One reciprocal for two quotients was
+// tried: it saves one special-function operation in four but needs six instructions more a pair to
+// keep infinities and NaN apart, and the kernels are bound by instructions, not by that unit.)
+__device__ __forceinline__ float rcp_mufu(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
-__device__ __forceinline__ void sigmoid_pair(float2& v, float2& s, float2& e) {
-    v = make_float2(hold(v.x), hold(v.y));
+__device__ __forceinline__ float2 sigmoid_pair(float2 v) {
     const float2 z = __fmul2_rn(v, make_float2(-kLog2e, -kLog2e));
-    e = make_float2(ex2_mufu(fminf(z.x, 63.f)), ex2_mufu(fminf(z.y, 63.f)));
-    const float2 a = __fadd2_rn(e, make_float2(1.f, 1.f));
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a.x * a.y));
-    s = __fmul2_rn(make_float2(r, r), make_float2(a.y, a.x));
+    const float2 a = __fadd2_rn(make_float2(ex2_mufu(z.x), ex2_mufu(z.y)), make_float2(1.f, 1.f));
+    return make_float2(rcp_mufu(a.x), rcp_mufu(a.y));
 }
-__device__ __forceinline__ float2 silu_pair(float2 v) {
-    float2 s, e;
-    sigmoid_pair(v, s, e);
-    return __fmul2_rn(v, s);
-}
+__device__ __forceinline__ float2 silu_pair(float2 v) { return __fmul2_rn(v, sigmoid_pair(v)); }
+__device__ __forceinline__ float silu_fast(float v) { return v * rcp_mufu(1.0f + ex2_mufu(-v * kLog2e)); }
 
-// v sigmoid(v).  exp(-v) overflows to infinity below -88, where the quotient is zero, as v sigmoid(v)
-// is to fp32's smallest normal number.
-__device__ __forceinline__ float silu_fast(float v) {
-    return v * __fdividef(1.0f, 1.0f + ex2_mufu(-v * kLog2e));
+// Row t (0..2^30) of an array whose rows lie ldb bytes apart (below 2^32): one 32 x 32 + 64 bit
+// multiply-add.
+template <typename T>
+__device__ __forceinline__ T* row_at(T* base, int t, unsigned ldb) {
+    return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(base) + (unsigned long long)(unsigned)t * ldb);
 }
 
 // ---------------------------------------------------------------- packed sequences

@@ -95,7 +95,7 @@ def conv_shape(S, **kw):
 BAD_CONV = [(dict(batch=-1), 1), (dict(seqlen=-1), 1), (dict(dim=0), 1), (dict(reserved=1), 1), (dict(flags=2), 1),
             (dict(width=1), 2), (dict(width=5), 2), (dict(io=2), 2), (dict(batch=65536), 2),
             (dict(seqlen=(1 << 30) + 1), 2), (dict(dim=(1 << 22) + 8), 2), (dict(batch=65535, seqlen=1 << 30), 2),
-            (dict(dim=60), 3), (dict(ldx=32), 1), (dict(ldy=68), 3), (dict(lddy=-64), 1), (dict(lddx=1 << 40), 1)]
+            (dict(dim=60), 3), (dict(ldx=32), 1), (dict(ldy=68), 3), (dict(lddy=-64), 1), (dict(lddx=1 << 40), 2)]
 
 
 @pytest.mark.parametrize("change,code", BAD_CONV)

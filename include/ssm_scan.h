@@ -515,17 +515,14 @@ int ssm_conv_step(const ssm_conv_serve* shape, const void* x, const float* w, co
  * x, delta_raw, z, y [rows, D], Bm, Cm [rows, N] io type; A_log [D, N], Dskip [D] fp32. */
 typedef struct ssm_scan_serve {
     int64_t rows, seqs, dim, dstate, slots; /* dim at most 2^20, N one of 4, 8, 16; else as above */
-    int64_t max_len; /* prompts: no sequence is longer; 0 = rows.  The time split is planned by it.
-                        Single tokens: must be 0 */
+    int64_t max_len; /* prompts: no sequence is longer (0 = rows); by it the call decides whether the
+                        lengths differ enough to start the longest first.  Single tokens: must be 0 */
     int64_t ldx, lddelta, ldz, ldb, ldc, ldy;
     int32_t io;             /* ssm_dtype */
     int32_t discretization; /* ssm_discretization */
 } ssm_scan_serve;
 
-/* Workspace bytes of ssm_scan_prompt (at least 256); 0 for an invalid shape. */
-size_t ssm_scan_prompt_workspace_bytes(const ssm_scan_serve* shape);
-
-/* Prompts.  Enqueues 1 kernel, or 3 when max_len is above the time segment that fills the GPU. */
+/* Prompts.  Enqueues 1 kernel. */
 int ssm_scan_prompt(const ssm_scan_serve* shape, const void* x, const void* delta_raw,
                     const float* A_log, const void* Bm, const void* Cm, const float* Dskip,
                     const void* z, const int32_t* offsets, const int32_t* slot,

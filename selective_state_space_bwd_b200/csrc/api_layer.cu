@@ -144,24 +144,6 @@ int check_scan_serve(const ssm_scan_serve* s, bool prompts) {
     return SSM_OK;
 }
 
-struct PromptPlan {
-    ssm::ScanServePlan p;
-    size_t sumP, sumS, end;
-};
-// SSM_ERR_UNSUPPORTED when the batch would need more CTAs than one launch holds.
-int plan_prompt(const ssm_scan_serve* s, PromptPlan* o) {
-    const int64_t max_len = s->max_len && s->max_len < s->rows ? s->max_len : s->rows;
-    o->p = ssm::plan_scan_prompt(s->rows, s->seqs, s->dim, (int)s->dstate, max_len);
-    if (o->p.items * ((s->dim + 31) / 32) > (int64_t)0x7fffffff) return SSM_ERR_UNSUPPORTED;
-    const size_t state = (size_t)s->dim * s->dstate * sizeof(float);
-    const size_t n = o->p.split ? (size_t)o->p.items * state : 0;
-    size_t off = kStatusBytes;
-    o->sumP = off; off = align256(off + n);
-    o->sumS = off; off = align256(off + n);
-    o->end = off;
-    return SSM_OK;
-}
-
 int scan_serve(const ssm_scan_serve* s, bool prompts, const void* x, const void* delta_raw,
                const float* A_log, const void* Bm, const void* Cm, const float* Dskip, const void* z,
                const int32_t* offsets, const int32_t* slot, const uint8_t* carry, float* pool,
@@ -180,12 +162,9 @@ int scan_serve(const ssm_scan_serve* s, bool prompts, const void* x, const void*
     const bool work = prompts ? s->seqs > 0 : rows > 0;
     if (work && (st = check_index(offsets, slot, prompts)) != SSM_OK) return st;
     if (!prompts && !slot && s->rows > s->slots) return SSM_ERR_INVALID_ARG;
-    PromptPlan p = {};
-    if (prompts && (st = plan_prompt(s, &p)) != SSM_OK) return st;
     ssm::ScanServeArgs a = {};
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    const size_t need = prompts ? p.end : kStatusBytes;
-    if ((st = reset_status(ws, ws_bytes, need, cs, &a.status)) != SSM_OK) return st;
+    if ((st = reset_status(ws, ws_bytes, kStatusBytes, cs, &a.status)) != SSM_OK) return st;
     if ((st = clear_status(a.status, cs)) != SSM_OK || !work) return st;
     a.rows = (int)rows; a.S = (int)s->seqs; a.D = (int)D; a.slots = (int)s->slots;
     a.max_len = s->max_len && s->max_len < s->rows ? (int)s->max_len : (int)rows;
@@ -195,10 +174,8 @@ int scan_serve(const ssm_scan_serve* s, bool prompts, const void* x, const void*
     a.ldb = stride(s->ldb, s->dstate); a.ldc = stride(s->ldc, s->dstate);
     a.x = x; a.draw = delta_raw; a.A_log = A_log; a.Bm = Bm; a.Cm = Cm; a.Dskip = Dskip; a.z = z;
     a.offsets = offsets; a.slot = slot; a.carry = carry; a.pool = pool; a.y = y;
-    if (!prompts) return launch_status(ssm::launch_scan_step(a, s->io == SSM_BF16, (int)N, cs));
-    a.G = p.p.G; a.split = p.p.split; a.items = p.p.items;
-    a.sumP = at<float>(ws, p.sumP); a.sumS = at<float>(ws, p.sumS);
-    return launch_status(ssm::launch_scan_prompt(a, s->io == SSM_BF16, (int)N, p.p.states, cs));
+    return launch_status(prompts ? ssm::launch_scan_prompt(a, s->io == SSM_BF16, (int)N, cs)
+                                 : ssm::launch_scan_step(a, s->io == SSM_BF16, (int)N, cs));
 }
 
 }  // namespace
@@ -290,12 +267,6 @@ int ssm_conv_step(const ssm_conv_serve* shape, const void* x, const float* w, co
                   const int32_t* slot, void* pool, void* y, void* ws, size_t ws_bytes,
                   ssm_stream_t stream) {
     return conv_serve(shape, false, x, w, bias, nullptr, slot, nullptr, pool, y, ws, ws_bytes, stream);
-}
-
-size_t ssm_scan_prompt_workspace_bytes(const ssm_scan_serve* shape) {
-    PromptPlan p;
-    if (check_scan_serve(shape, true) != SSM_OK || plan_prompt(shape, &p) != SSM_OK) return 0;
-    return p.end;
 }
 
 int ssm_scan_prompt(const ssm_scan_serve* shape, const void* x, const void* delta_raw,

@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_prompt_kernel(ConvServeArgs 
         check_batch(a.offsets, a.slot, a.S, a.rows, a.slots, a.rows, a.status);
     int s = find_seq(a.offsets, a.S, a.G, item0);
     for (int k = 0; k < ty && s + 1 < a.S && item_base(a.offsets, s + 1, a.G) <= item; ++k) ++s;
-    const Span sp = item_span(a.offsets, a.slot, s, a.G, item, a.rows, a.slots, a.rows);
+    const Span sp = item_span(a.offsets, a.slot, s, a.G, item, a.rows, a.slots);
     __syncthreads();
     if (sp.ok && ty < a.ry && named_before(a.slot, sp.s, sp.slot, tx, a.cx)) repeated[ty] = 1;
     __syncthreads();

@@ -130,20 +130,33 @@ __device__ __forceinline__ int find_seq(const int32_t* offsets, int S, int G, in
     return lo;
 }
 
-// The item's rows, with everything that the device must not trust checked.  Does not look for
+__device__ __forceinline__ int length_of(const int32_t* offsets, int s) {
+    return (int)((unsigned)offsets[s + 1] - (unsigned)offsets[s]);
+}
+
+// Sequence s's rows, with everything that the device must not trust checked.  Does not look for
 // repeated slots (see named_before).
-__device__ __forceinline__ Span item_span(const int32_t* offsets, const int32_t* slot, int s, int G,
-                                          int64_t item, int rows, int slots, int max_len) {
+__device__ __forceinline__ Span seq_span(const int32_t* offsets, const int32_t* slot, int s, int rows, int slots,
+                                         int max_len) {
     Span r;
-    r.s = s;
     const int o0 = offsets[s], o1 = offsets[s + 1];
-    const int64_t local = item - item_base(offsets, s, G);
+    r.s = s;
     r.slot = slot[s];
+    r.local = 0;
+    r.first = o0;
     r.end = o1;
-    const bool sane = o0 >= 0 && o0 <= o1 && o1 <= rows && o1 - o0 <= max_len && r.slot < slots;
-    r.ok = sane && local >= 0 && (local == 0 || local * G < o1 - o0);
+    r.ok = o0 >= 0 && o0 <= o1 && o1 <= rows && o1 - o0 <= max_len && r.slot < slots;
+    return r;
+}
+
+// An item's rows: one piece of sequence s.
+__device__ __forceinline__ Span item_span(const int32_t* offsets, const int32_t* slot, int s, int G,
+                                          int64_t item, int rows, int slots) {
+    Span r = seq_span(offsets, slot, s, rows, slots, rows);
+    const int64_t local = item - item_base(offsets, s, G);
+    r.ok = r.ok && local >= 0 && (local == 0 || local * G < r.end - r.first);
     r.local = r.ok ? (int)local : 0;
-    r.first = r.ok ? o0 + r.local * G : 0;
+    r.first = r.ok ? r.first + r.local * G : 0;
     return r;
 }
 

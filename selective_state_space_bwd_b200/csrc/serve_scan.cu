@@ -34,9 +34,6 @@ using real::ex2_pair;
 using real::f2;
 using real::kFull;
 
-constexpr int kTT = 32;   // steps per staged tile of B and C
-constexpr int kU = 8;     // steps per unrolled group
-constexpr int kThreads = 128;
 
 // four B or C elements of a row, as fp32
 template <typename E>
@@ -46,206 +43,247 @@ __device__ __forceinline__ float4 quad_f4(const typename Vec<E, 4>::Raw& r) {
     return make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
 }
 
-// w B x for a pair of states: (delta, delta x), a = exp(delta A), zl2 = delta A log2(e), Ar = 1 / A
+// w B x for a pair of states: delta and delta x (each twice), e = exp(delta A), A2 = A log2(e), Ar = 1 / A
 template <bool ZOH>
-__device__ __forceinline__ float2 input_term(float2 dd, float2 a, float2 zl2, float2 Ar, float2 bq) {
+__device__ __forceinline__ float2 input_term(float2 dlt, float2 dx, float2 e, float2 A2, float2 Ar, float2 bq) {
     if constexpr (ZOH) {
-        const float2 z = __fmul2_rn(zl2, f2(kLn2));
-        const float2 rz = __fmul2_rn(f2(__fdividef(1.0f, dd.x)), Ar);
-        return __fmul2_rn(__fmul2_rn(f2(dd.y), real::zoh_e1(z, a, rz)), bq);
+        const float2 z = __fmul2_rn(__fmul2_rn(dlt, A2), f2(kLn2));
+        const float2 rz = __fmul2_rn(f2(rcp_mufu(dlt.x)), Ar);
+        return __fmul2_rn(__fmul2_rn(dx, real::zoh_e1(z, e, rz)), bq);
     } else {
-        return __fmul2_rn(f2(dd.y), bq);
+        return __fmul2_rn(dx, bq);
     }
 }
 
-// S states from S/4 16-byte vectors
-template <int S>
-__device__ __forceinline__ void ld_state(float2 (&h)[S / 2], const float* p) {
-    real::ld_pairs<S>(h, p);
+// softplus_fast of a pair in packed arithmetic.
+__device__ __forceinline__ float2 softplus_pair(float2 v) {
+    const float2 z = __fmul2_rn(make_float2(fabsf(v.x), fabsf(v.y)), f2(-kLog2e));
+    const float2 e = ex2_pair(z), a = __fadd2_rn(e, f2(2.0f));
+    const float2 s = __fmul2_rn(e, make_float2(rcp_mufu(a.x), rcp_mufu(a.y))), w = __fmul2_rn(s, s);
+    float2 q = __ffma2_rn(w, f2(0.28011780977249146f), f2(0.2800184488296509f));
+    q = __ffma2_rn(w, q, f2(0.4002152383327484f));
+    q = __ffma2_rn(w, q, f2(0.666664183139801f));
+    q = __ffma2_rn(w, q, f2(2.0f));
+    return __ffma2_rn(s, q, make_float2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
 }
 
-template <typename E, int N, int S, bool ZOH, bool SUMMARY>
-__global__ void __launch_bounds__(kThreads) scan_prompt_kernel(ScanServeArgs a) {
-    constexpr int NG = N / S, DC = kThreads / NG, P2 = S / 2, SH = kU / NG;  // SH: steps of a lane's share
-    constexpr int NQ = kTT * N / 4;                                  // four-element vectors of a B tile
-    constexpr int PER = (NQ + kThreads - 1) / kThreads;
-    __shared__ __align__(16) float sB[2][kTT * N];
-    __shared__ __align__(16) float sC[SUMMARY ? 1 : 2][SUMMARY ? 4 : kTT * N];
-    const int64_t item = blockIdx.x / a.ndt;
-    const int tile = blockIdx.x % a.ndt;
-    const int tid = threadIdx.x, ng = tid % NG, dl = tid / NG;
-    const int d = tile * DC + dl, n0 = ng * S;
-    const bool dv = d < a.D;
+// Prompts.  A lane owns four states of two neighbouring channels: NG = N / 4 lanes a pair of channels, CW
+// channels a CTA.  Each of its warps holds all of them, for its turns of U steps.  Row by row a lane
+// holds SH of the turn's steps, the same ones whose sums the reduction over the NG lanes leaves in it.
+template <int N>
+struct PromptCfg {
+    static constexpr int NG = N / 4;
+    static constexpr int CW = 64 / NG;
+    static constexpr int U = N == 4 ? 4 : 8;
+    static constexpr int SH = U / NG;
+};
 
-    if (!SUMMARY && a.status && blockIdx.x == 0)
+// A pair of neighbouring channels as it lies in a row.
+template <typename E> struct Pair;
+template <> struct Pair<float> {
+    using Raw = float2;
+    static __device__ __forceinline__ float2 to_f(Raw r) { return r; }
+    static __device__ __forceinline__ Raw from_f(float2 v) { return v; }
+};
+template <> struct Pair<__nv_bfloat16> {
+    using Raw = unsigned;
+    static __device__ __forceinline__ float2 to_f(Raw r) { return bf16_pair(r); }
+    static __device__ __forceinline__ Raw from_f(float2 v) { return pack_bf16(v); }
+};
+
+// Hand-over between two warps: named barriers 1 .. NW, one per receiving warp.
+__device__ __forceinline__ void hand_wait(int w) { asm volatile("bar.sync %0, 64;" ::"r"(w + 1) : "memory"); }
+__device__ __forceinline__ void hand_over(int w) { asm volatile("bar.arrive %0, 64;" ::"r"(w + 1) : "memory"); }
+
+template <typename E, int N, bool ZOH, int NW>
+__global__ void __launch_bounds__(NW * 32, 12 / NW) scan_prompt_kernel(ScanServeArgs a) {
+    using Cfg = PromptCfg<N>;
+    using PR = typename Pair<E>::Raw;
+    using BR = typename Vec<E, 4>::Raw;
+    constexpr int NG = Cfg::NG, CW = Cfg::CW, U = Cfg::U, SH = Cfg::SH, NP = CW / 2;
+    __shared__ float2 s_dlt[NW][U][NP];         // delta and delta x of a pair of channels
+    __shared__ float2 s_dx[NW][U][NP];
+    __shared__ __align__(16) BR s_b[NW][U * NG], s_c[NW][U * NG];  // four states of a step, as loaded
+    __shared__ float4 s_h[NW][2][32];
+    __shared__ int s_seq;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ng = lane % NG, dl = lane / NG;
+    const int d = (int)(blockIdx.x % a.ndt) * CW + 2 * dl, n0 = ng * 4;  // the lane's channels d, d + 1
+    const bool dv = d < a.D;
+    const int dc = dv ? d : 0;  // lanes past the last channel run along on channel 0 and store nothing
+
+    float4 l[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) l[c] = __ldg(reinterpret_cast<const float4*>(a.A_log + (size_t)(dc + c) * N + n0));
+    if (a.status && blockIdx.x == 0)
         check_batch(a.offsets, a.slot, a.S, a.rows, a.slots, a.max_len, a.status);
-    const int s = find_seq(a.offsets, a.S, a.G, item);
-    const Span sp = item_span(a.offsets, a.slot, s, a.G, item, a.rows, a.slots, a.max_len);
+    const int rank = (int)(blockIdx.x / a.ndt);
+    int s = rank;
+    if (a.sorted) {  // the longest sequences first
+        const int j = threadIdx.x;
+        if (j < a.S) {
+            const int len = length_of(a.offsets, j);
+            int r = 0;
+            for (int i = 0; i < a.S; ++i) {
+                const int other = length_of(a.offsets, i);
+                r += other > len || (other == len && i < j);
+            }
+            if (r == rank) s_seq = j;
+        }
+        __syncthreads();
+        s = s_seq;
+    }
+    const Span sp = seq_span(a.offsets, a.slot, s, a.rows, a.slots, a.max_len);
     if (!sp.ok) return;  // the whole CTA
-    const int n = min(a.G, sp.end - sp.first);  // this segment's steps
-    const bool last = sp.first + n == sp.end;
-    if (SUMMARY && last) return;
-    if (__syncthreads_or(named_before(a.slot, s, sp.slot, tid, kThreads))) {
-        if (!SUMMARY && tid == 0) flag_if(a.status, kStatusInvalid);
+    const int n = sp.end - sp.first, turns = (n + U - 1) / U;
+
+    // the sequence's first row; rows are addressed by 32-bit byte strides
+    const size_t r0 = (size_t)sp.first;
+    const bool gated = a.z != nullptr;
+    const unsigned ldx = (unsigned)(a.ldx * sizeof(E)), ldd = (unsigned)(a.ldd * sizeof(E));
+    const unsigned ldz = (unsigned)(a.ldz * sizeof(E)), ldy = (unsigned)(a.ldy * sizeof(E));
+    const unsigned ldb = (unsigned)(a.ldb * sizeof(E)), ldc = (unsigned)(a.ldc * sizeof(E));
+    const E* px = static_cast<const E*>(a.x) + r0 * a.ldx + dc;
+    const E* pd = static_cast<const E*>(a.draw) + r0 * a.ldd + dc;
+    const E* pz = gated ? static_cast<const E*>(a.z) + r0 * a.ldz + dc : nullptr;
+    E* py = static_cast<E*>(a.y) + r0 * a.ldy + dc;
+    const int brow = lane / NG, bcol = (lane % NG) * 4;  // B and C: the first U * NG lanes
+    const E* pB = static_cast<const E*>(a.Bm) + r0 * a.ldb + bcol;
+    const E* pC = static_cast<const E*>(a.Cm) + r0 * a.ldc + bcol;
+
+    PR nx[SH], nd[SH], nz[SH];
+    BR nB, nC;
+    auto load = [&](int t) {  // past the end: the last row again
+#pragma unroll
+        for (int k = 0; k < SH; ++k) {
+            const int r = min(t + ng * SH + k, n - 1);
+            nx[k] = *reinterpret_cast<const PR*>(row_at(px, r, ldx));
+            nd[k] = *reinterpret_cast<const PR*>(row_at(pd, r, ldd));
+            if (gated) nz[k] = *reinterpret_cast<const PR*>(row_at(pz, r, ldz));
+        }
+        if (lane < U * NG) {
+            const int r = min(t + brow, n - 1);
+            nB = ld_vec<E, 4>(row_at(pB, r, ldb));
+            nC = ld_vec<E, 4>(row_at(pC, r, ldc));
+        }
+    };
+    if (warp < turns) load(warp * U);
+    if (__syncthreads_or(named_before(a.slot, s, sp.slot, threadIdx.x, NW * 32))) {
+        if (threadIdx.x == 0) flag_if(a.status, kStatusInvalid);
         return;
     }
-
-    float2 A2[P2], Ar[P2], h[P2];
+    float2 A2[2][2], Ar[2][2];  // [channel][pair of states]
 #pragma unroll
-    for (int i = 0; i < P2; ++i) {
-        const float l0 = dv ? a.A_log[(size_t)d * N + n0 + 2 * i] : 0.f;
-        const float l1 = dv ? a.A_log[(size_t)d * N + n0 + 2 * i + 1] : 0.f;
-        A2[i] = make_float2(-expf(l0) * kLog2e, -expf(l1) * kLog2e);
-        if (ZOH) Ar[i] = make_float2(-expf(-l0), -expf(-l1));
-        h[i] = f2(0.f);
-    }
-    float* entry = sp.slot >= 0 ? a.pool + ((size_t)sp.slot * a.D + d) * N + n0 : nullptr;
-    if (!SUMMARY && dv) {
-        if (sp.local > 0)  // the carry's state entering this segment
-            ld_state<S>(h, a.sumS + ((size_t)item * a.D + d) * N + n0);
-        else if (entry && a.carry && a.carry[s])
-            ld_state<S>(h, entry);
-    }
-    const float dsk = !SUMMARY && dv ? a.Dskip[d] : 0.f;
-    float dsum = 0.f;  // summary: sum of delta over the lane's own steps
-
-    const size_t r0 = (size_t)sp.first;
-    const E* px = static_cast<const E*>(a.x) + r0 * a.ldx + (dv ? d : 0);
-    const E* pd = static_cast<const E*>(a.draw) + r0 * a.ldd + (dv ? d : 0);
-    const E* pz = !SUMMARY && a.z ? static_cast<const E*>(a.z) + r0 * a.ldz + (dv ? d : 0) : nullptr;
-    E* py = SUMMARY ? nullptr : static_cast<E*>(a.y) + r0 * a.ldy + d;
-    const E* pB = static_cast<const E*>(a.Bm) + r0 * a.ldb;
-    const E* pC = static_cast<const E*>(a.Cm) + r0 * a.ldc;
-
-    // B and C of steps [t, t + 32): zero past the segment's end, so that a step which is not there
-    // (delta = 0: transition one) adds nothing to the state
-    typename Vec<E, 4>::Raw rB[PER], rC[PER];
-    auto fetch = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int q = tid + i * kThreads, row = q / (N / 4), col = (q % (N / 4)) * 4;
-            const bool ok = q < NQ && t + row < n;
-            rB[i] = ok ? ld_vec<E, 4>(pB + (size_t)(t + row) * a.ldb + col) : Vec<E, 4>::zero();
-            if (!SUMMARY) rC[i] = ok ? ld_vec<E, 4>(pC + (size_t)(t + row) * a.ldc + col) : Vec<E, 4>::zero();
-        }
-    };
-    auto stage = [&](int k) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int q = tid + i * kThreads;
-            if (q < NQ) {
-                reinterpret_cast<float4*>(sB[k])[q] = quad_f4<E>(rB[i]);
-                if (!SUMMARY) reinterpret_cast<float4*>(sC[SUMMARY ? 0 : k])[q] = quad_f4<E>(rC[i]);
-            }
-        }
-    };
-    // the lane's share of the group at t: steps t + ng * SH + j
-    E nx[SH], nd[SH], nz[SH];
-    auto next = [&](int t) {
-#pragma unroll
-        for (int j = 0; j < SH; ++j) {
-            const int r = t + ng * SH + j;
-            const bool ok = r < n;
-            nx[j] = ok ? px[(size_t)r * a.ldx] : Elem<E>::from_f(0.f);
-            nd[j] = ok ? pd[(size_t)r * a.ldd] : Elem<E>::from_f(0.f);
-            if (!SUMMARY) nz[j] = ok && pz ? pz[(size_t)r * a.ldz] : Elem<E>::from_f(0.f);
-        }
-    };
-
-    fetch(0);
-    next(0);
-    for (int t0 = 0, k = 0; t0 < n; t0 += kTT, k ^= 1) {
-        stage(k);
-        __syncthreads();  // also: everyone has left the tile before last, whose buffer is next
-        if (t0 + kTT < n) fetch(t0 + kTT);
-        const int tend = min(n, t0 + kTT);
-        for (int t = t0; t < tend; t += kU) {
-            float dlt[SH], dx[SH], xs[SH], zs[SH];
-#pragma unroll
-            for (int j = 0; j < SH; ++j) {
-                const bool ok = t + ng * SH + j < n;
-                xs[j] = Elem<E>::to_f(nx[j]);
-                zs[j] = SUMMARY ? 0.f : Elem<E>::to_f(nz[j]);
-                dlt[j] = ok ? softplus_fast(Elem<E>::to_f(nd[j])) : 0.f;
-                dx[j] = dlt[j] * xs[j];
-                if (SUMMARY) dsum += dlt[j];
-            }
-            next(t + kU);
-            float yp[kU];
-            const float* tB = sB[k] + (t - t0) * N + n0;
-            const float* tC = sC[SUMMARY ? 0 : k] + (SUMMARY ? 0 : (t - t0) * N + n0);
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                float2 dd = make_float2(dlt[u % SH], dx[u % SH]);
-                if (NG > 1) {
-                    dd.x = __shfl_sync(kFull, dd.x, u / SH, NG);
-                    dd.y = __shfl_sync(kFull, dd.y, u / SH, NG);
-                }
-                float2 bq[P2], cq[P2], acc = f2(0.f);
-                real::ld_pairs<S>(bq, tB + u * N);
-                if (!SUMMARY) real::ld_pairs<S>(cq, tC + u * N);
-#pragma unroll
-                for (int i = 0; i < P2; ++i) {
-                    const float2 zl2 = __fmul2_rn(f2(dd.x), A2[i]);
-                    const float2 e = ex2_pair(zl2);
-                    h[i] = __ffma2_rn(e, h[i], input_term<ZOH>(dd, e, zl2, Ar[i], bq[i]));
-                    if (!SUMMARY) acc = __ffma2_rn(cq[i], h[i], acc);
-                }
-                yp[u] = acc.x + acc.y;
-            }
-            if (!SUMMARY) {
-                real::reduce_scatter<kU, NG>(yp, ng);
-#pragma unroll
-                for (int j = 0; j < SH; ++j) {
-                    const int r = t + ng * SH + j;
-                    float v = fmaf(dsk, xs[j], yp[j]);
-                    if (pz) v *= silu_fast(zs[j]);
-                    if (dv && r < n) py[(size_t)r * a.ldy] = Elem<E>::from_f(v);
-                }
-            }
+    for (int c = 0; c < 2; ++c) {
+        A2[c][0] = make_float2(-expf(l[c].x) * kLog2e, -expf(l[c].y) * kLog2e);
+        A2[c][1] = make_float2(-expf(l[c].z) * kLog2e, -expf(l[c].w) * kLog2e);
+        if (ZOH) {
+            Ar[c][0] = make_float2(-expf(-l[c].x), -expf(-l[c].y));
+            Ar[c][1] = make_float2(-expf(-l[c].z), -expf(-l[c].w));
         }
     }
-    if (SUMMARY) {
-        // the product of the transitions is exp(A sum delta): the lanes' sums, added over the channel
+    const float2 dsk = *reinterpret_cast<const float2*>(a.Dskip + dc);
+    float* entry = sp.slot >= 0 && dv ? a.pool + ((size_t)sp.slot * a.D + d) * N + n0 : nullptr;
+    float4 h4[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (warp == 0 && entry) {
+        if (a.carry && a.carry[s])
 #pragma unroll
-        for (int m = 1; m < NG; m <<= 1) dsum += __shfl_xor_sync(kFull, dsum, m);
-        if (dv) {
-            float2 P[P2];
+            for (int c = 0; c < 2; ++c) h4[c] = *reinterpret_cast<const float4*>(entry + c * N);
+        if (turns == 0)
 #pragma unroll
-            for (int i = 0; i < P2; ++i) P[i] = ex2_pair(__fmul2_rn(f2(dsum), A2[i]));
-            const size_t o = ((size_t)item * a.D + d) * N + n0;
-            real::st_pairs<S>(a.sumP + o, P);
-            real::st_pairs<S>(a.sumS + o, h);
-        }
-    } else if (dv && last) {
-        if (entry) real::st_pairs<S>(entry, h);
-        if (!real::all_finite<S>(h)) flag_if(a.status, kStatusNonFinite);
+            for (int c = 0; c < 2; ++c) *reinterpret_cast<float4*>(entry + c * N) = h4[c];
     }
-}
 
-// The states entering the segments of each sequence, written over the segments' end states (segment
-// i's entering state in place of segment i's own sum): four states a thread.
-__global__ void __launch_bounds__(256) scan_carry_kernel(ScanServeArgs a, int DN4) {
-    const int s = blockIdx.y, k = blockIdx.x * 256 + threadIdx.x;
-    const int64_t base = item_base(a.offsets, s, a.G);
-    const Span sp = item_span(a.offsets, a.slot, s, a.G, base, a.rows, a.slots, a.max_len);
-    const int len = sp.ok ? sp.end - sp.first : 0;
-    const int nseg = (len + a.G - 1) / a.G;
-    if (nseg < 2) return;  // the whole CTA: nothing to carry
-    if (__syncthreads_or(named_before(a.slot, s, sp.slot, threadIdx.x, 256))) return;
-    if (k >= DN4) return;
-    float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (sp.slot >= 0 && a.carry && a.carry[s])
-        h = reinterpret_cast<const float4*>(a.pool)[(size_t)sp.slot * DN4 + k];
-    const float4* P = reinterpret_cast<const float4*>(a.sumP) + (size_t)base * DN4 + k;
-    float4* E = reinterpret_cast<float4*>(a.sumS) + (size_t)base * DN4 + k;
-#pragma unroll 4
-    for (int i = 0; i < nseg; ++i) {
-        float4 p, e;
-        if (i + 1 < nseg) { p = P[(size_t)i * DN4]; e = E[(size_t)i * DN4]; }
-        E[(size_t)i * DN4] = h;
-        if (i + 1 < nseg)
-            h = make_float4(fmaf(p.x, h.x, e.x), fmaf(p.y, h.y, e.y), fmaf(p.z, h.z, e.z), fmaf(p.w, h.w, e.w));
+    for (int i = warp; i < turns; i += NW) {
+        const int t = i * U;
+        // delta and delta x of the turn, the steps side by side
+        float2 x[SH], z[SH];
+#pragma unroll
+        for (int k = 0; k < SH; ++k) {
+            const int u = ng * SH + k;
+            x[k] = Pair<E>::to_f(nx[k]);
+            if (gated) z[k] = Pair<E>::to_f(nz[k]);
+            float2 dl2 = softplus_pair(Pair<E>::to_f(nd[k])), dx2 = __fmul2_rn(dl2, x[k]);
+            if (t + u >= n) dl2 = dx2 = f2(0.f);  // a step that is not there changes nothing
+            s_dlt[warp][u][dl] = dl2;
+            s_dx[warp][u][dl] = dx2;
+        }
+        if (lane < U * NG) {
+            s_b[warp][lane] = t + brow < n ? nB : Vec<E, 4>::zero();
+            s_c[warp][lane] = t + brow < n ? nC : Vec<E, 4>::zero();
+        }
+        __syncwarp();
+        if (i + NW < turns) load(t + NW * U);
+        // the transitions: nothing here waits for the state
+        float2 e[U][2][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float2 dlt = s_dlt[warp][u][dl];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                e[u][0][p] = ex2_pair(__fmul2_rn(f2(dlt.x), A2[0][p]));
+                e[u][1][p] = ex2_pair(__fmul2_rn(f2(dlt.y), A2[1][p]));
+            }
+        }
+        // the recurrence, from the warp before to the warp after; e[u] becomes the state at step u
+        if (i > 0) {
+            hand_wait(warp);
+            h4[0] = s_h[warp][0][lane];
+            h4[1] = s_h[warp][1][lane];
+        }
+        float2 h[2][2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            h[c][0] = make_float2(h4[c].x, h4[c].y);
+            h[c][1] = make_float2(h4[c].z, h4[c].w);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float2 bq[2];
+            Vec<E, 4>::unpack(s_b[warp][u * NG + ng], bq);
+            const float2 dx = s_dx[warp][u][dl];
+            float2 dlt = f2(0.f);
+            if (ZOH) dlt = s_dlt[warp][u][dl];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const float2 w0 = input_term<ZOH>(f2(dlt.x), f2(dx.x), e[u][0][p], A2[0][p], Ar[0][p], bq[p]);
+                const float2 w1 = input_term<ZOH>(f2(dlt.y), f2(dx.y), e[u][1][p], A2[1][p], Ar[1][p], bq[p]);
+                h[0][p] = e[u][0][p] = __ffma2_rn(e[u][0][p], h[0][p], w0);
+                h[1][p] = e[u][1][p] = __ffma2_rn(e[u][1][p], h[1][p], w1);
+            }
+        }
+        if (i + 1 < turns) {
+            const int to = warp + 1 == NW ? 0 : warp + 1;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) s_h[to][c][lane] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
+            hand_over(to);
+        } else {
+            if (entry)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    *reinterpret_cast<float4*>(entry + c * N) = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
+            if (dv && !(real::all_finite<4>(h[0]) && real::all_finite<4>(h[1]))) flag_if(a.status, kStatusNonFinite);
+        }
+        // y: the lane's part of the sums over the states, then their reduction
+        float yp[2 * U];  // [step][channel]
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float2 cq[2];
+            Vec<E, 4>::unpack(s_c[warp][u * NG + ng], cq);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float2 acc = __ffma2_rn(cq[1], e[u][c][1], __fmul2_rn(cq[0], e[u][c][0]));
+                yp[2 * u + c] = acc.x + acc.y;
+            }
+        }
+        real::reduce_scatter<2 * U, NG>(yp, ng);
+#pragma unroll
+        for (int k = 0; k < SH; ++k) {
+            const int r = t + ng * SH + k;
+            float2 v = __ffma2_rn(dsk, x[k], make_float2(yp[2 * k], yp[2 * k + 1]));
+            if (gated) v = __fmul2_rn(v, silu_pair(z[k]));
+            if (dv && r < n) *reinterpret_cast<PR*>(row_at(py, r, ldy)) = Pair<E>::from_f(v);
+        }
+        __syncwarp();
     }
 }
 
@@ -317,7 +355,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanServeArgs a) {
         for (int i = 0; i < 2; ++i) {
             const float2 zl2 = __fmul2_rn(f2(dd.x), A2[i]);
             const float2 e = ex2_pair(zl2);
-            h[i] = __ffma2_rn(e, h[i], input_term<ZOH>(dd, e, zl2, Ar[i], bq[i]));
+            h[i] = __ffma2_rn(e, h[i], input_term<ZOH>(f2(dd.x), f2(dd.y), e, A2[i], Ar[i], bq[i]));
             acc = __ffma2_rn(cq[i], h[i], acc);
         }
         float v = acc.x + acc.y;
@@ -335,34 +373,30 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanServeArgs a) {
     }
 }
 
-template <typename E, int N, int S, bool ZOH>
+template <typename E, int N, bool ZOH>
 cudaError_t prompt_impl(ScanServeArgs a, cudaStream_t st) {
-    constexpr int DC = kThreads / (N / S);
-    a.ndt = (a.D + DC - 1) / DC;
-    const unsigned grid = (unsigned)(a.items * a.ndt);
-    cudaError_t e;
-    if (a.split) {
-        scan_prompt_kernel<E, N, S, ZOH, true><<<grid, kThreads, 0, st>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        const int DN4 = a.D * (N / 4);
-        scan_carry_kernel<<<dim3((DN4 + 255) / 256, a.S), 256, 0, st>>>(a, DN4);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    scan_prompt_kernel<E, N, S, ZOH, false><<<grid, kThreads, 0, st>>>(a);
+    constexpr int CW = PromptCfg<N>::CW;
+    a.ndt = (a.D + CW - 1) / CW;
+    const int64_t ctas = (int64_t)a.S * a.ndt;
+    // worth it when there are more CTAs than run at once, and few enough sequences to be ranked by every CTA
+    a.sorted = a.S > 1 && a.S <= 64 && ctas > 296 && (int64_t)a.max_len * a.S > 2 * (int64_t)a.rows;
+    if (ctas <= 148)
+        scan_prompt_kernel<E, N, ZOH, 12><<<(unsigned)ctas, 12 * 32, 0, st>>>(a);
+    else
+        scan_prompt_kernel<E, N, ZOH, 6><<<(unsigned)ctas, 6 * 32, 0, st>>>(a);
     return cudaGetLastError();
 }
 
 template <typename E, int N>
-cudaError_t prompt_pick(const ScanServeArgs& a, int states, cudaStream_t st) {
-    if (states == N) return a.zoh ? prompt_impl<E, N, N, true>(a, st) : prompt_impl<E, N, N, false>(a, st);
-    return a.zoh ? prompt_impl<E, N, 4, true>(a, st) : prompt_impl<E, N, 4, false>(a, st);
+cudaError_t prompt_pick(const ScanServeArgs& a, cudaStream_t st) {
+    return a.zoh ? prompt_impl<E, N, true>(a, st) : prompt_impl<E, N, false>(a, st);
 }
 
 template <typename E>
-cudaError_t prompt_dispatch(const ScanServeArgs& a, int N, int states, cudaStream_t st) {
-    if (N == 4) return prompt_pick<E, 4>(a, states, st);
-    if (N == 8) return prompt_pick<E, 8>(a, states, st);
-    return prompt_pick<E, 16>(a, states, st);
+cudaError_t prompt_dispatch(const ScanServeArgs& a, int N, cudaStream_t st) {
+    if (N == 4) return prompt_pick<E, 4>(a, st);
+    if (N == 8) return prompt_pick<E, 8>(a, st);
+    return prompt_pick<E, 16>(a, st);
 }
 
 template <typename E, int N, int R>
@@ -394,25 +428,9 @@ cudaError_t step_dispatch(const ScanServeArgs& a, int N, cudaStream_t st) {
 }  // namespace
 }  // namespace serve
 
-ScanServePlan plan_scan_prompt(int64_t rows, int64_t S, int64_t D, int N, int64_t max_len) {
-    ScanServePlan p;
-    p.states = 4;
-    const int64_t dc = serve::kThreads / (N / p.states), ndt = (D + dc - 1) / dc;
-    // steps of one of 1184 CTAs (8 per SM) if the batch were spread evenly
-    const int64_t even = rows * ndt / 1184;
-    int64_t G = max_len;
-    if (max_len > 2 * even && max_len > 128) G = (even > 64 ? even : 64);
-    G = (G + 31) / 32 * 32;
-    if (G < 32) G = 32;
-    p.G = (int)G;
-    p.split = max_len > G;
-    p.items = rows / G + S;
-    return p;
-}
-
-cudaError_t launch_scan_prompt(const ScanServeArgs& a, int io_bf16, int N, int states, cudaStream_t st) {
-    return io_bf16 ? serve::prompt_dispatch<__nv_bfloat16>(a, N, states, st)
-                   : serve::prompt_dispatch<float>(a, N, states, st);
+cudaError_t launch_scan_prompt(const ScanServeArgs& a, int io_bf16, int N, cudaStream_t st) {
+    return io_bf16 ? serve::prompt_dispatch<__nv_bfloat16>(a, N, st)
+                   : serve::prompt_dispatch<float>(a, N, st);
 }
 
 cudaError_t launch_scan_step(const ScanServeArgs& a, int io_bf16, int N, cudaStream_t st) {

@@ -213,9 +213,8 @@ cudaError_t launch_conv_step(const ConvServeArgs& a, int width, bool silu, int i
 // Scan over packed prompts and single tokens (csrc/serve_scan.cu).
 struct ScanServeArgs {
     int rows, S, D, slots, max_len, zoh;
-    int G, split;         // rows a time segment; split: sequences of several segments may occur
     int ndt;              // channel tiles
-    int64_t items;
+    int sorted;           // prompts: the longest sequences first
     size_t ldx, ldd, ldz, ldb, ldc, ldy;
     const void* x;
     const void* draw;
@@ -229,16 +228,9 @@ struct ScanServeArgs {
     const uint8_t* carry;
     float* pool;
     void* y;
-    float* sumP;          // per item [items][D][N]: the segment's transition product, and its end
-    float* sumS;          //   state from zero, which the carry replaces by the state entering it
     unsigned* status;     // or null
 };
-struct ScanServePlan {
-    int G, split, states; // states: states a thread owns
-    int64_t items;
-};
-ScanServePlan plan_scan_prompt(int64_t rows, int64_t S, int64_t D, int N, int64_t max_len);
-cudaError_t launch_scan_prompt(const ScanServeArgs& a, int io_bf16, int N, int states, cudaStream_t st);
+cudaError_t launch_scan_prompt(const ScanServeArgs& a, int io_bf16, int N, cudaStream_t st);
 cudaError_t launch_scan_step(const ScanServeArgs& a, int io_bf16, int N, cudaStream_t st);
 
 // Launchers (return cudaGetLastError() of the last launch).

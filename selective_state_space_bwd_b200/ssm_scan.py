@@ -101,7 +101,7 @@ EXPORTED = ["ssm_scan_abi_version", "ssm_scan_checkpoint_bytes", "ssm_scan_works
             "ssm_pdssm_workspace_bytes", "ssm_pdssm_fwd", "ssm_pdssm_bwd",
             "ssm_pdssm_kernel_launches", "ssm_dtproj_workspace_bytes", "ssm_dtproj_fwd",
             "ssm_dtproj_bwd", "ssm_conv_fwd", "ssm_conv_restore", "ssm_conv_workspace_bytes",
-            "ssm_conv_bwd", "ssm_conv_prompt", "ssm_conv_step", "ssm_scan_prompt_workspace_bytes",
+            "ssm_conv_bwd", "ssm_conv_prompt", "ssm_conv_step",
             "ssm_scan_prompt", "ssm_scan_step"]
 
 
@@ -169,8 +169,6 @@ def lib():
             L.ssm_conv_bwd.argtypes, L.ssm_conv_bwd.restype = [KP] + [P] * 13 + [Z, P], I
             L.ssm_conv_prompt.argtypes, L.ssm_conv_prompt.restype = [VP] + [P] * 9 + [Z, P], I
             L.ssm_conv_step.argtypes, L.ssm_conv_step.restype = [VP] + [P] * 7 + [Z, P], I
-            L.ssm_scan_prompt_workspace_bytes.argtypes = [GP]
-            L.ssm_scan_prompt_workspace_bytes.restype = Z
             L.ssm_scan_prompt.argtypes, L.ssm_scan_prompt.restype = [GP] + [P] * 13 + [Z, P], I
             L.ssm_scan_step.argtypes, L.ssm_scan_step.restype = [GP] + [P] * 11 + [Z, P], I
             _lib = L
@@ -677,10 +675,6 @@ def conv_workspace_bytes(shape: SsmConvShape) -> int:
     return int(lib().ssm_conv_workspace_bytes(ctypes.byref(shape)))
 
 
-def scan_prompt_workspace_bytes(shape: SsmScanServe) -> int:
-    return int(lib().ssm_scan_prompt_workspace_bytes(ctypes.byref(shape)))
-
-
 def conv_shape(batch, seqlen, dim, width, io=SSM_BF16, silu=True, ldx=0, ldy=0, lddy=0, lddx=0):
     return SsmConvShape(int(batch), int(seqlen), int(dim), int(ldx), int(ldy), int(lddy), int(lddx),
                         int(width), int(io), SSM_CONV_SILU if silu else 0, 0)
@@ -880,15 +874,13 @@ def _scan_serve(name, x, delta_raw, A_log, Bm, Cm, Dskip, offsets, slots, pool, 
     else:
         seqs = 0
         _expect(slots, "slots", (rows,), torch.int32, dev)
+    wp, wn = _ws_args(ws, dev)
     with _On(dev, stream):
         if y is None:
             y = torch.empty((rows, D), dtype=dt, device=dev)
         ldy = _expect_rows(y, "y", x.shape, dt, dev)
         shape = SsmScanServe(rows, seqs, D, N, pool.shape[0], int(max_len), ldx, ldd, ldz, ldb, ldc,
                              ldy, io, SSM_ZOH if zoh else SSM_EULER)
-        if offsets is not None and ws is None:
-            ws = _workspace(scan_prompt_workspace_bytes(shape), dev, None)
-        wp, wn = _ws_args(ws, dev)
         if offsets is not None:
             code = lib().ssm_scan_prompt(shape, x.data_ptr(), delta_raw.data_ptr(), A_log.data_ptr(),
                                          Bm.data_ptr(), Cm.data_ptr(), Dskip.data_ptr(), _ptr0(z),
@@ -908,7 +900,8 @@ def ssm_scan_prompt(x, delta_raw, A_log, Bm, Cm, Dskip, offsets, slots, pool, ca
     """Scan of packed prompts from and to a pool of states [slots, D, N] fp32 (updated in place), y
     times SiLU(z) when z is given.  x, delta_raw, z [R,D], Bm, Cm [R,N] in one io type, rows may be
     strided; offsets, slots, carry as for ssm_conv_prompt; ``max_len`` bounds the sequences' length
-    (0: the rows) and decides the time split.  Returns y [R,D]."""
+    (0: the rows; a longer one is left out).  ``ws`` (256 bytes, optional) receives the status word.
+    Returns y [R,D]."""
     if offsets is None:
         raise ValueError("offsets is needed")
     return _scan_serve("ssm_scan_prompt", x, delta_raw, A_log, Bm, Cm, Dskip, offsets, slots, pool,

@@ -152,7 +152,6 @@ COMMON = [(dict(rows=-1), 1), (dict(seqs=-1), 1), (dict(slots=-1), 1), (dict(dim
 def test_scan_serve_shapes_refused(S, change, code):
     L, s = S.lib(), scan_serve(S, **change)
     assert L.ssm_scan_prompt(s, *[P] * 7, P, P, P, P, 2 * P, 3 * P, 1 << 40, None) == code
-    assert L.ssm_scan_prompt_workspace_bytes(s) == 0
     s = scan_serve(S, **{"seqs": 0, **change})
     assert L.ssm_scan_step(s, *[P] * 7, P, P, 2 * P, None, 0, None) == (1 if change.get("seqs") else code)
 
@@ -169,7 +168,7 @@ def test_conv_serve_shapes_refused(S, change, code):
 def test_serving_pointers_refused(S):
     L = S.lib()
     s = scan_serve(S)
-    need = L.ssm_scan_prompt_workspace_bytes(s)
+    need = 256
     #       x  dr A  B  C  D  z  off slot carry pool y      ws     n
     base = [P, P, P, P, P, P, P, P, P, P, P, 2 * P, 3 * P, need]
     for i, v, code in [(0, None, 1), (1, P + 8, 3), (2, None, 1), (3, P + 4, 3), (4, None, 1), (5, P + 8, 3),
@@ -188,17 +187,6 @@ def test_serving_pointers_refused(S):
     assert L.ssm_conv_step(s, P, P, P, None, P, 2 * P, None, 0, None) == 1
     assert L.ssm_conv_step(s, P, P, P, P, P, P, None, 0, None) == 1  # y on x
     assert L.ssm_conv_prompt(conv_serve(S), P, P, P, None, P, P, P, 2 * P, None, 0, None) == 1
-
-
-def test_prompt_workspace_follows_the_time_split(S):
-    """No split: the status word alone.  Split: two states an item, items at most rows / G + S."""
-    L = S.lib()
-    assert L.ssm_scan_prompt_workspace_bytes(scan_serve(S, rows=100, seqs=5)) == 256
-    one = scan_serve(S, rows=8192, seqs=1, dim=1536)
-    n = L.ssm_scan_prompt_workspace_bytes(one)
-    state = 1536 * 16 * 4
-    assert (n - 256) % (2 * state) == 0 and 2 <= (n - 256) // (2 * state) <= 8192 // 32 + 1
-    assert L.ssm_scan_prompt_workspace_bytes(scan_serve(S, rows=1 << 16, seqs=512, dim=1536, max_len=200)) == 256
 
 
 # ---------------------------------------------------------------- host models
@@ -262,6 +250,48 @@ def test_backward_pieces_write_every_gradient_once(L, G, W):
                 for k in range(W):  # g of rows r..r+W-1: zero before the start and past the end
                     assert r + k < 0 or r + k >= L or t0 <= r + k < tend
     assert (summed == 1).all() and wrote == {r: 1 for r in range(-(W - 1), L)}
+
+
+@pytest.mark.parametrize("turns", list(range(0, 20)) + [64, 100])
+@pytest.mark.parametrize("seed", range(3))
+def test_warps_hand_the_state_over_without_a_deadlock(turns, seed):
+    """The prompt scan's ring of eight warps under random scheduling: one barrier per receiving warp,
+    a hand-over is complete when one arrival and one wait have met on it.  Every turn runs once and in
+    order, no arrival meets another arrival on its barrier, no slot is written before it was read, and all
+    warps come to their end."""
+    rng = np.random.default_rng(seed)
+    W = 8
+    arrived, slot, order = [False] * W, [None] * W, []
+
+    def warp(w):
+        for i in range(w, turns, W):
+            yield "work"
+            if i > 0:
+                while not arrived[w]:
+                    yield "wait"
+                arrived[w] = False
+                assert slot[w] == i - 1
+                slot[w] = None
+            order.append(i)
+            yield "chain"
+            if i + 1 < turns:
+                to = (w + 1) % W
+                assert slot[to] is None and not arrived[to]
+                slot[to] = i
+                yield "stored"
+                arrived[to] = True
+            yield "output"
+    live = {w: warp(w) for w in range(W)}
+    idle = 0
+    while live:
+        w = int(rng.choice(list(live)))
+        try:
+            idle = idle + 1 if next(live[w]) == "wait" else 0
+        except StopIteration:
+            del live[w]
+            idle = 0
+        assert idle < 10000
+    assert order == list(range(turns)) and not any(arrived)
 
 
 def test_ctypes_structs_have_the_header_sizes(S):

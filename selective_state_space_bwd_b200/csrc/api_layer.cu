@@ -135,6 +135,8 @@ int check_scan_serve(const ssm_scan_serve* s, bool prompts) {
     if (int st = check_rows(s->rows, s->seqs, s->slots, prompts)) return st;
     if (check_io(s->io) != SSM_OK || s->dim > (int64_t)1 << 20) return SSM_ERR_UNSUPPORTED;
     if (s->dstate != 4 && s->dstate != 8 && s->dstate != 16) return SSM_ERR_UNSUPPORTED;
+    const int64_t tile = 256 / s->dstate;  // channels of a prompt CTA: the grid holds 2^31 - 1 CTAs
+    if (s->seqs * ((s->dim + tile - 1) / tile) > (int64_t)0x7fffffff) return SSM_ERR_UNSUPPORTED;
     const int64_t unit = 16 / esize(s->io);
     if (s->dim % unit != 0) return SSM_ERR_MISALIGNED;
     for (int64_t ld : {s->ldx, s->lddelta, s->ldz, s->ldy})

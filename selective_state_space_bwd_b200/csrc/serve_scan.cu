@@ -4,23 +4,17 @@
 //     h_t = exp(delta_t A) h_{t-1} + w_t B_t x_t,   y_t = (C_t . h_t + D x_t) [z_t sigmoid(z_t)],
 //     w = delta (Euler) or (exp(delta A) - 1) / A (zero-order hold).
 //
-// Prompts.  What bounds a long prompt is the exp2 unit: one exp2 a state and step (16 lanes a
-// cycle and SM, so 8 cycles a warp instruction) against 4 packed fp32 instructions for two states;
-// memory traffic is 8 bytes a channel and step in bf16, a small share.  So nothing may stand between
-// the exp2s: a warp needs no other warp except for B and C, which a CTA converts to fp32 in shared
-// memory once for its channels, double-buffered, one barrier per 32 steps.  A channel's N states
-// are spread over NG adjacent lanes; a lane reads x, delta and z of its share of eight steps straight
-// from global memory (one group ahead), evaluates their softplus and gate once, hands (delta,
-// delta x) to its neighbours by shuffles, and the reduce-scatter of the eight y's over the lanes
-// leaves each lane the y's of the same steps, so y is gated and stored by the lane that holds z.
-// With NG = 1 (all states in one thread) there are no shuffles and the fewest instructions a state;
-// with NG = N / 4 a batch has four times the threads.
-//
-// Time split.  A sequence longer than G rows runs as segments: a first launch scans every segment
-// but the last from zero (end state and transition product), the carry turns these into the
-// states entering the segments, and the scan runs from them.  That evaluates every exp2 of a
-// split sequence twice, so it is done only when the unsplit batch would leave the GPU waiting for
-// its longest sequence (plan_scan_prompt).
+// Prompts.  One exp2 a state and step bounds them from below (16 lanes a cycle and SM, so 8 cycles a warp
+// instruction); next come shared memory (B, C, delta for every lane: one wavefront a cycle and SM)
+// and the issue slots.  Memory traffic, 8 bytes a channel and step in bf16, is a small share.  The
+// recurrence itself is short, but serial, and everything else is not.  So a CTA takes a few channels of one
+// whole sequence, and its warps take turns of U steps in a ring: a warp loads its turn one round
+// ahead, computes transitions and input terms of all U steps, then waits for the state from the warp
+// before, runs its U steps, hands the state on through shared memory and a named barrier, and finishes its y's
+// while the others go on.  A sequence of any length is one pass: nothing is evaluated twice, no segment
+// summaries, no workspace, and the result does not depend on a split.  (Measured before: time segments
+// with summaries and a carry, which evaluate every exp2 twice: 4096 steps of 1536 channels took 98 us
+// against 86, a ragged batch of 24 prompts on 4096 channels 445 us against 325.)
 //
 // Single tokens.  Bound by the states' traffic, 8 N bytes a channel and row.
 #include "layer_common.cuh"
@@ -68,14 +62,23 @@ __device__ __forceinline__ float2 softplus_pair(float2 v) {
 }
 
 // Prompts.  A lane owns four states of two neighbouring channels: NG = N / 4 lanes a pair of channels, CW
-// channels a CTA.  Each of its warps holds all of them, for its turns of U steps.  Row by row a lane
-// holds SH of the turn's steps, the same ones whose sums the reduction over the NG lanes leaves in it.
-template <int N>
+// channels a CTA.  Each of its NW warps holds all of them, for its turns of U steps.  Row by row a lane
+// holds SH of a turn's steps, the same ones whose sums the reduction over the NG lanes leaves in it.
+// Three forms, chosen by prompt_impl:
+//   kMany: turns of four steps, four warps a CTA, four CTAs an SM, which share it.
+//   kFew: turns of eight steps, eight warps and one CTA an SM: fewer hand-overs a step.
+//   kAlone: as kFew, but what counts is how soon a warp hands the state on, so a turn is first reduced to
+//   h_out = P h_in + S (more arithmetic, but off the chain from warp to warp).
+enum Form { kMany, kFew, kAlone };
+template <int N, int FORM>
 struct PromptCfg {
+    static constexpr bool MANY = FORM == kMany;
     static constexpr int NG = N / 4;
     static constexpr int CW = 64 / NG;
-    static constexpr int U = N == 4 ? 4 : 8;
+    static constexpr int U = MANY ? 4 : 8;
+    static constexpr int NW = MANY ? 4 : 8;
     static constexpr int SH = U / NG;
+    static constexpr int kCtas = MANY ? 4 : 1;   // an SM
 };
 
 // A pair of neighbouring channels as it lies in a row.
@@ -95,12 +98,14 @@ template <> struct Pair<__nv_bfloat16> {
 __device__ __forceinline__ void hand_wait(int w) { asm volatile("bar.sync %0, 64;" ::"r"(w + 1) : "memory"); }
 __device__ __forceinline__ void hand_over(int w) { asm volatile("bar.arrive %0, 64;" ::"r"(w + 1) : "memory"); }
 
-template <typename E, int N, bool ZOH, int NW>
-__global__ void __launch_bounds__(NW * 32, 12 / NW) scan_prompt_kernel(ScanServeArgs a) {
-    using Cfg = PromptCfg<N>;
+template <typename E, int N, bool ZOH, int FORM>
+__global__ void __launch_bounds__(PromptCfg<N, FORM>::NW * 32, PromptCfg<N, FORM>::kCtas)
+scan_prompt_kernel(ScanServeArgs a) {
+    using Cfg = PromptCfg<N, FORM>;
+    constexpr bool ALONE = FORM == kAlone;
     using PR = typename Pair<E>::Raw;
     using BR = typename Vec<E, 4>::Raw;
-    constexpr int NG = Cfg::NG, CW = Cfg::CW, U = Cfg::U, SH = Cfg::SH, NP = CW / 2;
+    constexpr int NG = Cfg::NG, CW = Cfg::CW, U = Cfg::U, SH = Cfg::SH, NP = CW / 2, NW = Cfg::NW;
     __shared__ float2 s_dlt[NW][U][NP];         // delta and delta x of a pair of channels
     __shared__ float2 s_dx[NW][U][NP];
     __shared__ __align__(16) BR s_b[NW][U * NG], s_c[NW][U * NG];  // four states of a step, as loaded
@@ -213,18 +218,37 @@ __global__ void __launch_bounds__(NW * 32, 12 / NW) scan_prompt_kernel(ScanServe
         }
         __syncwarp();
         if (i + NW < turns) load(t + NW * U);
-        // the transitions: nothing here waits for the state
-        float2 e[U][2][2];
+        // transitions and input terms: nothing here waits for the state
+        float2 e[U][2][2], w[U][2][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float2 dlt = s_dlt[warp][u][dl];
+            const float2 dlt = s_dlt[warp][u][dl], dx = s_dx[warp][u][dl];
+            float2 bq[2];
+            Vec<E, 4>::unpack(s_b[warp][u * NG + ng], bq);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 e[u][0][p] = ex2_pair(__fmul2_rn(f2(dlt.x), A2[0][p]));
                 e[u][1][p] = ex2_pair(__fmul2_rn(f2(dlt.y), A2[1][p]));
+                w[u][0][p] = input_term<ZOH>(f2(dlt.x), f2(dx.x), e[u][0][p], A2[0][p], Ar[0][p], bq[p]);
+                w[u][1][p] = input_term<ZOH>(f2(dlt.y), f2(dx.y), e[u][1][p], A2[1][p], Ar[1][p], bq[p]);
             }
         }
-        // the recurrence, from the warp before to the warp after; e[u] becomes the state at step u
+        float2 P[2][2], out[2][2];  // the turn as a whole: out = P h + out
+        if (ALONE) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    P[c][p] = e[0][c][p];
+                    out[c][p] = w[0][c][p];
+#pragma unroll
+                    for (int u = 1; u < U; ++u) {
+                        P[c][p] = __fmul2_rn(P[c][p], e[u][c][p]);
+                        out[c][p] = __ffma2_rn(e[u][c][p], out[c][p], w[u][c][p]);
+                    }
+                }
+        }
+        // from the warp before
         if (i > 0) {
             hand_wait(warp);
             h4[0] = s_h[warp][0][lane];
@@ -236,33 +260,36 @@ __global__ void __launch_bounds__(NW * 32, 12 / NW) scan_prompt_kernel(ScanServe
             h[c][0] = make_float2(h4[c].x, h4[c].y);
             h[c][1] = make_float2(h4[c].z, h4[c].w);
         }
+        auto recur = [&]() {  // e[u] becomes the state at step u
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float2 bq[2];
-            Vec<E, 4>::unpack(s_b[warp][u * NG + ng], bq);
-            const float2 dx = s_dx[warp][u][dl];
-            float2 dlt = f2(0.f);
-            if (ZOH) dlt = s_dlt[warp][u][dl];
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const float2 w0 = input_term<ZOH>(f2(dlt.x), f2(dx.x), e[u][0][p], A2[0][p], Ar[0][p], bq[p]);
-                const float2 w1 = input_term<ZOH>(f2(dlt.y), f2(dx.y), e[u][1][p], A2[1][p], Ar[1][p], bq[p]);
-                h[0][p] = e[u][0][p] = __ffma2_rn(e[u][0][p], h[0][p], w0);
-                h[1][p] = e[u][1][p] = __ffma2_rn(e[u][1][p], h[1][p], w1);
-            }
-        }
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) h[c][p] = e[u][c][p] = __ffma2_rn(e[u][c][p], h[c][p], w[u][c][p]);
+        };
+        if (!ALONE) recur();
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) out[c][p] = !ALONE ? h[c][p] : __ffma2_rn(P[c][p], h[c][p], out[c][p]);
+        // to the warp after
         if (i + 1 < turns) {
             const int to = warp + 1 == NW ? 0 : warp + 1;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) s_h[to][c][lane] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
+            for (int c = 0; c < 2; ++c)
+                s_h[to][c][lane] = make_float4(out[c][0].x, out[c][0].y, out[c][1].x, out[c][1].y);
             hand_over(to);
         } else {
             if (entry)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                    *reinterpret_cast<float4*>(entry + c * N) = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
-            if (dv && !(real::all_finite<4>(h[0]) && real::all_finite<4>(h[1]))) flag_if(a.status, kStatusNonFinite);
+                    *reinterpret_cast<float4*>(entry + c * N) =
+                        make_float4(out[c][0].x, out[c][0].y, out[c][1].x, out[c][1].y);
+            if (dv && !(real::all_finite<4>(out[0]) && real::all_finite<4>(out[1])))
+                flag_if(a.status, kStatusNonFinite);
         }
+        if (ALONE) recur();
         // y: the lane's part of the sums over the states, then their reduction
         float yp[2 * U];  // [step][channel]
 #pragma unroll
@@ -288,103 +315,199 @@ __global__ void __launch_bounds__(NW * 32, 12 / NW) scan_prompt_kernel(ScanServe
 }
 
 // ---------------------------------------------------------------- single tokens
-// Four states a thread, N / 4 lanes a channel, R rows a CTA: the transition's A is computed once
-// for the R rows and their states are in flight together.  Lane ng of a channel evaluates the softplus
-// and the gate of row ng (R <= N / 4 lanes) and hands them to its neighbours.
-template <typename E, int N, int R, bool ZOH>
+// Four states a thread, N / 4 lanes a channel.
+struct StepRow {  // what one row adds to the state
+    float2 A2[2], Ar[2];
+    float dsk;
+};
+
+template <bool ZOH>
+__device__ __forceinline__ StepRow step_consts(float4 l, float dsk) {
+    StepRow c;
+    c.A2[0] = make_float2(-expf(l.x) * kLog2e, -expf(l.y) * kLog2e);
+    c.A2[1] = make_float2(-expf(l.z) * kLog2e, -expf(l.w) * kLog2e);
+    if (ZOH) {
+        c.Ar[0] = make_float2(-expf(-l.x), -expf(-l.y));
+        c.Ar[1] = make_float2(-expf(-l.z), -expf(-l.w));
+    }
+    c.dsk = dsk;
+    return c;
+}
+
+// h <- exp(delta A) h + w B x; returns (the channel's) y before the gate, in every lane of the channel.
+template <typename E, int NG, bool ZOH>
+__device__ __forceinline__ float step_row(const StepRow& c, float2 (&h)[2], E x, E dr,
+                                          typename Vec<E, 4>::Raw rB, typename Vec<E, 4>::Raw rC) {
+    const float xf = Elem<E>::to_f(x);
+    const float dlt = softplus_fast(Elem<E>::to_f(dr)), dx = dlt * xf;
+    float2 bq[2], cq[2], acc = f2(0.f);
+    Vec<E, 4>::unpack(rB, bq);
+    Vec<E, 4>::unpack(rC, cq);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 e = ex2_pair(__fmul2_rn(f2(dlt), c.A2[i]));
+        h[i] = __ffma2_rn(e, h[i], input_term<ZOH>(f2(dlt), f2(dx), e, c.A2[i], c.Ar[i], bq[i]));
+        acc = __ffma2_rn(cq[i], h[i], acc);
+    }
+    float v = acc.x + acc.y;
+#pragma unroll
+    for (int m = 1; m < NG; m <<= 1) v += __shfl_xor_sync(kFull, v, m);
+    return fmaf(c.dsk, xf, v);
+}
+
+// One row a CTA, every load in flight at once: the shortest way for few rows.
+template <typename E, int N, bool ZOH>
 __global__ void __launch_bounds__(256) scan_step_kernel(ScanServeArgs a) {
     constexpr int NG = N / 4, DC = 256 / NG;
     const int tid = threadIdx.x, ng = tid % NG, dl = tid / NG, n0 = ng * 4;
-    const int d = blockIdx.x * DC + dl;
+    const int d = blockIdx.x * DC + dl, row = blockIdx.y;
     const bool dv = d < a.D;
-    const int row0 = blockIdx.y * R;
-
-    int k[R];
-    float4 h4[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int row = row0 + r;
-        k[r] = row < a.rows ? (a.slot ? a.slot[row] : row) : -1;
-        const bool work = dv && k[r] >= 0 && k[r] < a.slots;
-        h4[r] = work ? *reinterpret_cast<const float4*>(a.pool + ((size_t)k[r] * a.D + d) * N + n0)
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
+    const int dc = dv ? d : 0;
+    const float4 l = __ldg(reinterpret_cast<const float4*>(a.A_log + (size_t)dc * N + n0));
+    const float dsk = a.Dskip[dc];
+    const int k = a.slot ? a.slot[row] : row;
+    const bool live = k >= 0 && k < a.slots, work = dv && live;
+    typename Vec<E, 4>::Raw rB = Vec<E, 4>::zero(), rC = Vec<E, 4>::zero();
+    E x = Elem<E>::from_f(0.f), dr = x, z = x;
+    if (live) {  // a padding row is not read
+        rB = ld_vec<E, 4>(static_cast<const E*>(a.Bm) + row * a.ldb + n0);
+        rC = ld_vec<E, 4>(static_cast<const E*>(a.Cm) + row * a.ldc + n0);
+        x = static_cast<const E*>(a.x)[row * a.ldx + dc];
+        dr = static_cast<const E*>(a.draw)[row * a.ldd + dc];
+        if (a.z) z = static_cast<const E*>(a.z)[row * a.ldz + dc];
     }
-    typename Vec<E, 4>::Raw rB[R], rC[R];
-    E x[R], dr[R], z[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const bool work = dv && k[r] >= 0 && k[r] < a.slots;
-        const size_t row = work ? row0 + r : 0;
-        rB[r] = work ? ld_vec<E, 4>(static_cast<const E*>(a.Bm) + row * a.ldb + n0) : Vec<E, 4>::zero();
-        rC[r] = work ? ld_vec<E, 4>(static_cast<const E*>(a.Cm) + row * a.ldc + n0) : Vec<E, 4>::zero();
-        x[r] = work ? static_cast<const E*>(a.x)[row * a.ldx + d] : Elem<E>::from_f(0.f);
-        dr[r] = work ? static_cast<const E*>(a.draw)[row * a.ldd + d] : Elem<E>::from_f(0.f);
-        z[r] = work && a.z ? static_cast<const E*>(a.z)[row * a.ldz + d] : Elem<E>::from_f(0.f);
+    float* entry = a.pool + ((size_t)(live ? k : 0) * a.D + dc) * N + n0;
+    const float4 h4 = work ? *reinterpret_cast<const float4*>(entry) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool repeated = a.slot && __syncthreads_or(named_before(a.slot, row, live ? k : -1, tid, 256));
+    if (k >= a.slots || repeated) {
+        if (tid == 0 && blockIdx.x == 0) flag_if(a.status, kStatusInvalid);
+        return;
     }
-    const float4 l = dv ? __ldg(reinterpret_cast<const float4*>(a.A_log + (size_t)d * N + n0))
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float dsk = dv ? a.Dskip[d] : 0.f;
-    if (a.slot) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const bool in = k[r] >= 0 && k[r] < a.slots;
-            const bool rep = __syncthreads_or(named_before(a.slot, row0 + r, in ? k[r] : -1, tid, 256));
-            if (rep || k[r] >= a.slots) {
-                if (tid == 0 && blockIdx.x == 0) flag_if(a.status, kStatusInvalid);
-                k[r] = -1;
-            }
-        }
-    }
-    const float2 A2[2] = {make_float2(-expf(l.x) * kLog2e, -expf(l.y) * kLog2e),
-                          make_float2(-expf(l.z) * kLog2e, -expf(l.w) * kLog2e)};
-    float2 Ar[2];
-    if (ZOH) {
-        Ar[0] = make_float2(-expf(-l.x), -expf(-l.y));
-        Ar[1] = make_float2(-expf(-l.z), -expf(-l.w));
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const float xf = Elem<E>::to_f(x[r]);
-        const float dlt = softplus_fast(Elem<E>::to_f(dr[r]));
-        const float2 dd = make_float2(dlt, dlt * xf);
-        float2 bq[2], cq[2], acc = f2(0.f);
-        Vec<E, 4>::unpack(rB[r], bq);
-        Vec<E, 4>::unpack(rC[r], cq);
-        float2 h[2] = {make_float2(h4[r].x, h4[r].y), make_float2(h4[r].z, h4[r].w)};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float2 zl2 = __fmul2_rn(f2(dd.x), A2[i]);
-            const float2 e = ex2_pair(zl2);
-            h[i] = __ffma2_rn(e, h[i], input_term<ZOH>(f2(dd.x), f2(dd.y), e, A2[i], Ar[i], bq[i]));
-            acc = __ffma2_rn(cq[i], h[i], acc);
-        }
-        float v = acc.x + acc.y;
-#pragma unroll
-        for (int m = 1; m < NG; m <<= 1) v += __shfl_xor_sync(kFull, v, m);
-        if (!dv || k[r] < 0) continue;
-        *reinterpret_cast<float4*>(a.pool + ((size_t)k[r] * a.D + d) * N + n0) =
-            make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
-        if (!real::all_finite<4>(h)) flag_if(a.status, kStatusNonFinite);
-        if (ng == 0) {
-            v = fmaf(dsk, xf, v);
-            if (a.z) v *= silu_fast(Elem<E>::to_f(z[r]));
-            static_cast<E*>(a.y)[(size_t)(row0 + r) * a.ldy + d] = Elem<E>::from_f(v);
-        }
+    const StepRow c = step_consts<ZOH>(l, dsk);
+    float2 h[2] = {make_float2(h4.x, h4.y), make_float2(h4.z, h4.w)};
+    float v = step_row<E, NG, ZOH>(c, h, x, dr, rB, rC);
+    if (!work) return;
+    *reinterpret_cast<float4*>(entry) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+    if (!real::all_finite<4>(h)) flag_if(a.status, kStatusNonFinite);
+    if (ng == 0) {
+        if (a.z) v *= silu_fast(Elem<E>::to_f(z));
+        static_cast<E*>(a.y)[row * a.ldy + d] = Elem<E>::from_f(v);
     }
 }
 
+// Up to kStepRows rows a CTA.  The states' traffic is all that counts, so each thread keeps the states of
+// two groups of four rows on their way (cp.async into its own places of a ring), and the rest of the next
+// group in registers, while it computes a group; A is computed once for all rows.
+constexpr int kStepRows = 64, kStepStages = 3, kStepGroup = 4;
+
+template <typename E, int N, bool ZOH>
+__global__ void __launch_bounds__(256, 2) scan_step_batch_kernel(ScanServeArgs a, int rows_per_cta) {
+    constexpr int NG = N / 4, DC = 256 / NG, R = kStepGroup;
+    extern __shared__ __align__(16) unsigned char smem[];
+    float4* ring = reinterpret_cast<float4*>(smem) + threadIdx.x;  // slot i: ring[i * 256]
+    __shared__ int s_slot[kStepRows];                              // -1: leave the row alone
+    const int tid = threadIdx.x, ng = tid % NG, dl = tid / NG, n0 = ng * 4;
+    const int d = blockIdx.x * DC + dl;
+    const bool dv = d < a.D;
+    const int dc = dv ? d : 0;
+    const int row0 = blockIdx.y * rows_per_cta, nrows = min(rows_per_cta, a.rows - row0);
+    const float4 l = __ldg(reinterpret_cast<const float4*>(a.A_log + (size_t)dc * N + n0));
+    const float dsk = a.Dskip[dc];
+    if (tid < kStepRows) {
+        const int k = tid < nrows ? (a.slot ? a.slot[row0 + tid] : row0 + tid) : -1;
+        if (k >= a.slots && blockIdx.x == 0) flag_if(a.status, kStatusInvalid);
+        s_slot[tid] = k < a.slots ? k : -1;
+    }
+    __syncthreads();
+    if (a.slot) {  // rows that name an entry which an earlier row names: 256 / kStepRows threads a row
+        constexpr int TR = 256 / kStepRows;
+        const int r = tid / TR, k = s_slot[r];
+        const bool hit = named_before(a.slot, row0 + r, k, tid % TR, TR);
+        __syncthreads();
+        if (hit) {
+            s_slot[r] = -1;
+            if (blockIdx.x == 0) flag_if(a.status, kStatusInvalid);
+        }
+        __syncthreads();
+    }
+    auto issue = [&](int r, int stage) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (r + i < nrows && s_slot[r + i] >= 0)
+                real::cp_async16(ring + (stage * R + i) * 256,
+                                 a.pool + ((size_t)s_slot[r + i] * a.D + dc) * N + n0, true);
+        real::cp_async_commit();
+    };
+    typename Vec<E, 4>::Raw nB[R], nC[R];
+    E nx[R], nd[R], nz[R];
+    auto fetch = [&](int r) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            nx[i] = nd[i] = nz[i] = Elem<E>::from_f(0.f);
+            nB[i] = nC[i] = Vec<E, 4>::zero();
+            if (r + i < nrows && s_slot[r + i] >= 0) {
+                const size_t row = row0 + r + i;
+                nB[i] = ld_vec<E, 4>(static_cast<const E*>(a.Bm) + row * a.ldb + n0);
+                nC[i] = ld_vec<E, 4>(static_cast<const E*>(a.Cm) + row * a.ldc + n0);
+                nx[i] = static_cast<const E*>(a.x)[row * a.ldx + dc];
+                nd[i] = static_cast<const E*>(a.draw)[row * a.ldd + dc];
+                if (a.z) nz[i] = static_cast<const E*>(a.z)[row * a.ldz + dc];
+            }
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kStepStages - 1; ++i) issue(i * R, i);
+    fetch(0);
+    const StepRow c = step_consts<ZOH>(l, dsk);
+    int stage = 0;
+    for (int r = 0; r < nrows; r += R) {
+        typename Vec<E, 4>::Raw rB[R], rC[R];
+        E x[R], dr[R], z[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) { rB[i] = nB[i]; rC[i] = nC[i]; x[i] = nx[i]; dr[i] = nd[i]; z[i] = nz[i]; }
+        issue(r + (kStepStages - 1) * R, stage == 0 ? kStepStages - 1 : stage - 1);
+        fetch(r + R);
+        real::cp_async_wait<kStepStages - 1>();
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int k = r + i < nrows ? s_slot[r + i] : -1;
+            if (k < 0) continue;  // the whole CTA
+            const float4 h4 = ring[(stage * R + i) * 256];
+            float2 h[2] = {make_float2(h4.x, h4.y), make_float2(h4.z, h4.w)};
+            float v = step_row<E, NG, ZOH>(c, h, x[i], dr[i], rB[i], rC[i]);
+            if (!dv) continue;
+            *reinterpret_cast<float4*>(a.pool + ((size_t)k * a.D + d) * N + n0) =
+                make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+            if (!real::all_finite<4>(h)) flag_if(a.status, kStatusNonFinite);
+            if (ng == 0) {
+                if (a.z) v *= silu_fast(Elem<E>::to_f(z[i]));
+                static_cast<E*>(a.y)[(size_t)(row0 + r + i) * a.ldy + d] = Elem<E>::from_f(v);
+            }
+        }
+        stage = stage == kStepStages - 1 ? 0 : stage + 1;
+    }
+}
+
+template <typename E, int N, bool ZOH, int FORM>
+cudaError_t prompt_launch(const ScanServeArgs& a, unsigned ctas, cudaStream_t st) {
+    scan_prompt_kernel<E, N, ZOH, FORM><<<ctas, PromptCfg<N, FORM>::NW * 32, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+// Measured on a B200 (N = 16, bf16, gated), in cycles a step of 16 channels: a CTA alone on its SM takes 130
+// (kMany), 42 (kFew) and 36 (kAlone); an SM full of CTAs 36 (kMany) and 53 (kFew).  kFew wins while its
+// throughput, 53 rows ndt / 148, stays below the time that the longest sequence takes in kMany,
+// 130 max_len: rows * ndt < 363 max_len.  kAlone wins while every CTA has an SM to itself.
 template <typename E, int N, bool ZOH>
 cudaError_t prompt_impl(ScanServeArgs a, cudaStream_t st) {
-    constexpr int CW = PromptCfg<N>::CW;
-    a.ndt = (a.D + CW - 1) / CW;
+    a.ndt = (a.D + PromptCfg<N, kMany>::CW - 1) / PromptCfg<N, kMany>::CW;
     const int64_t ctas = (int64_t)a.S * a.ndt;
     // worth it when there are more CTAs than run at once, and few enough sequences to be ranked by every CTA
-    a.sorted = a.S > 1 && a.S <= 64 && ctas > 296 && (int64_t)a.max_len * a.S > 2 * (int64_t)a.rows;
-    if (ctas <= 148)
-        scan_prompt_kernel<E, N, ZOH, 12><<<(unsigned)ctas, 12 * 32, 0, st>>>(a);
-    else
-        scan_prompt_kernel<E, N, ZOH, 6><<<(unsigned)ctas, 6 * 32, 0, st>>>(a);
-    return cudaGetLastError();
+    a.sorted = a.S > 1 && a.S <= 64 && ctas > 592 && (int64_t)a.max_len * a.S > 2 * (int64_t)a.rows;
+    if (ctas <= 148) return prompt_launch<E, N, ZOH, kAlone>(a, (unsigned)ctas, st);
+    if ((int64_t)a.rows * a.ndt < (int64_t)363 * a.max_len)
+        return prompt_launch<E, N, ZOH, kFew>(a, (unsigned)ctas, st);
+    return prompt_launch<E, N, ZOH, kMany>(a, (unsigned)ctas, st);
 }
 
 template <typename E, int N>
@@ -399,23 +522,31 @@ cudaError_t prompt_dispatch(const ScanServeArgs& a, int N, cudaStream_t st) {
     return prompt_pick<E, 16>(a, st);
 }
 
-template <typename E, int N, int R>
+// One row a CTA while those CTAs run at once (8 an SM); else as many rows a CTA as leave one wave of two
+// CTAs an SM, in whole groups, at most kStepRows.
+template <typename E, int N, bool ZOH>
 cudaError_t step_impl(const ScanServeArgs& a, cudaStream_t st) {
     constexpr int DC = 256 / (N / 4);
-    const dim3 grid((a.D + DC - 1) / DC, (a.rows + R - 1) / R);
-    if (a.zoh)
-        scan_step_kernel<E, N, R, true><<<grid, 256, 0, st>>>(a);
-    else
-        scan_step_kernel<E, N, R, false><<<grid, 256, 0, st>>>(a);
+    const int64_t tiles = (a.D + DC - 1) / DC;
+    if (tiles * a.rows <= 1184) {
+        scan_step_kernel<E, N, ZOH><<<dim3((unsigned)tiles, a.rows), 256, 0, st>>>(a);
+    } else {
+        const int64_t groups = tiles < 296 ? 296 / tiles : 1;
+        int64_t rows = ((a.rows + groups - 1) / groups + kStepGroup - 1) / kStepGroup * kStepGroup;
+        if (rows > kStepRows) rows = kStepRows;
+        const int smem = kStepStages * kStepGroup * 256 * 16;
+        const cudaError_t e = cudaFuncSetAttribute(scan_step_batch_kernel<E, N, ZOH>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        scan_step_batch_kernel<E, N, ZOH>
+            <<<dim3((unsigned)tiles, (unsigned)((a.rows + rows - 1) / rows)), 256, smem, st>>>(a, (int)rows);
+    }
     return cudaGetLastError();
 }
 
 template <typename E, int N>
 cudaError_t step_pick(const ScanServeArgs& a, cudaStream_t st) {
-    // four rows a CTA once one row a CTA gives more CTAs than are resident (8 per SM)
-    constexpr int DC = 256 / (N / 4);
-    if ((int64_t)((a.D + DC - 1) / DC) * a.rows > 1184) return step_impl<E, N, 4>(a, st);
-    return step_impl<E, N, 1>(a, st);
+    return a.zoh ? step_impl<E, N, true>(a, st) : step_impl<E, N, false>(a, st);
 }
 
 template <typename E>

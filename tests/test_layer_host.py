@@ -253,14 +253,14 @@ def test_backward_pieces_write_every_gradient_once(L, G, W):
 
 
 @pytest.mark.parametrize("turns", list(range(0, 20)) + [64, 100])
+@pytest.mark.parametrize("W", [4, 8])
 @pytest.mark.parametrize("seed", range(3))
-def test_warps_hand_the_state_over_without_a_deadlock(turns, seed):
-    """The prompt scan's ring of eight warps under random scheduling: one barrier per receiving warp,
+def test_warps_hand_the_state_over_without_a_deadlock(turns, W, seed):
+    """The prompt scan's ring of warps under random scheduling: one barrier per receiving warp,
     a hand-over is complete when one arrival and one wait have met on it.  Every turn runs once and in
     order, no arrival meets another arrival on its barrier, no slot is written before it was read, and all
     warps come to their end."""
     rng = np.random.default_rng(seed)
-    W = 8
     arrived, slot, order = [False] * W, [None] * W, []
 
     def warp(w):

@@ -395,16 +395,25 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanServeArgs a) {
     }
 }
 
-// Up to kStepRows rows a CTA.  The states' traffic is all that counts, so each thread keeps the states of
-// two groups of four rows on their way (cp.async into its own places of a ring), and the rest of the next
-// group in registers, while it computes a group; A is computed once for all rows.
+// Up to kStepRows rows a CTA, in groups of four.  The states' traffic is all that should count, so each
+// thread keeps the states of two groups on their way (cp.async into its own places of a ring) while it
+// computes a third, and the instructions a row are kept few: A once for all rows, B and C once in fp32 in shared
+// memory, softplus, gate and y of a row in one of the channel's NG lanes each (lane ng: rows ng * SH ..).
 constexpr int kStepRows = 64, kStepStages = 3, kStepGroup = 4;
+
+template <int N>
+struct StepCfg {
+    static constexpr int oBC = kStepStages * kStepGroup * 256 * 16;
+    static constexpr int kBytes = oBC + 2 * kStepRows * N * 4;
+};
 
 template <typename E, int N, bool ZOH>
 __global__ void __launch_bounds__(256, 2) scan_step_batch_kernel(ScanServeArgs a, int rows_per_cta) {
-    constexpr int NG = N / 4, DC = 256 / NG, R = kStepGroup;
+    constexpr int NG = N / 4, DC = 256 / NG, R = kStepGroup, SH = R / NG;
     extern __shared__ __align__(16) unsigned char smem[];
     float4* ring = reinterpret_cast<float4*>(smem) + threadIdx.x;  // slot i: ring[i * 256]
+    float4* sB = reinterpret_cast<float4*>(smem + StepCfg<N>::oBC);  // [row][NG], then C the same
+    float4* sC = sB + kStepRows * NG;
     __shared__ int s_slot[kStepRows];                              // -1: leave the row alone
     const int tid = threadIdx.x, ng = tid % NG, dl = tid / NG, n0 = ng * 4;
     const int d = blockIdx.x * DC + dl;
@@ -421,8 +430,8 @@ __global__ void __launch_bounds__(256, 2) scan_step_batch_kernel(ScanServeArgs a
     __syncthreads();
     if (a.slot) {  // rows that name an entry which an earlier row names: 256 / kStepRows threads a row
         constexpr int TR = 256 / kStepRows;
-        const int r = tid / TR, k = s_slot[r];
-        const bool hit = named_before(a.slot, row0 + r, k, tid % TR, TR);
+        const int r = tid / TR;
+        const bool hit = named_before(a.slot, row0 + r, s_slot[r], tid % TR, TR);
         __syncthreads();
         if (hit) {
             s_slot[r] = -1;
@@ -430,62 +439,99 @@ __global__ void __launch_bounds__(256, 2) scan_step_batch_kernel(ScanServeArgs a
         }
         __syncthreads();
     }
+    float* pool = a.pool + (size_t)dc * N + n0;
+    const unsigned entry = (unsigned)((size_t)a.D * N * sizeof(float));  // bytes; below 2^27
     auto issue = [&](int r, int stage) {
 #pragma unroll
-        for (int i = 0; i < R; ++i)
-            if (r + i < nrows && s_slot[r + i] >= 0)
-                real::cp_async16(ring + (stage * R + i) * 256,
-                                 a.pool + ((size_t)s_slot[r + i] * a.D + dc) * N + n0, true);
-        real::cp_async_commit();
-    };
-    typename Vec<E, 4>::Raw nB[R], nC[R];
-    E nx[R], nd[R], nz[R];
-    auto fetch = [&](int r) {
-#pragma unroll
         for (int i = 0; i < R; ++i) {
-            nx[i] = nd[i] = nz[i] = Elem<E>::from_f(0.f);
-            nB[i] = nC[i] = Vec<E, 4>::zero();
-            if (r + i < nrows && s_slot[r + i] >= 0) {
-                const size_t row = row0 + r + i;
-                nB[i] = ld_vec<E, 4>(static_cast<const E*>(a.Bm) + row * a.ldb + n0);
-                nC[i] = ld_vec<E, 4>(static_cast<const E*>(a.Cm) + row * a.ldc + n0);
-                nx[i] = static_cast<const E*>(a.x)[row * a.ldx + dc];
-                nd[i] = static_cast<const E*>(a.draw)[row * a.ldd + dc];
-                if (a.z) nz[i] = static_cast<const E*>(a.z)[row * a.ldz + dc];
-            }
+            const int k = r + i < nrows ? s_slot[r + i] : -1;
+            if (k >= 0) real::cp_async16(ring + (stage * R + i) * 256, row_at(pool, k, entry), true);
         }
+        real::cp_async_commit();
     };
 #pragma unroll
     for (int i = 0; i < kStepStages - 1; ++i) issue(i * R, i);
+    // the lane's rows of a group: r + ng * SH + j
+    const unsigned ldx = (unsigned)(a.ldx * sizeof(E)), ldd = (unsigned)(a.ldd * sizeof(E));
+    const unsigned ldz = (unsigned)(a.ldz * sizeof(E)), ldy = (unsigned)(a.ldy * sizeof(E));
+    const E* px = static_cast<const E*>(a.x) + row0 * a.ldx + dc;
+    const E* pd = static_cast<const E*>(a.draw) + row0 * a.ldd + dc;
+    const E* pz = a.z ? static_cast<const E*>(a.z) + row0 * a.ldz + dc : nullptr;
+    E* py = static_cast<E*>(a.y) + row0 * a.ldy + dc;
+    E nx[SH], nd[SH], nz[SH];
+    int nk[SH];
+    auto fetch = [&](int r0) {  // a padding row is not read
+#pragma unroll
+        for (int j = 0; j < SH; ++j) {
+            const int r = r0 + ng * SH + j;
+            nk[j] = r < nrows ? s_slot[r] : -1;
+            nx[j] = nd[j] = nz[j] = Elem<E>::from_f(0.f);
+            if (nk[j] >= 0) {
+                nx[j] = *row_at(px, r, ldx);
+                nd[j] = *row_at(pd, r, ldd);
+                if (pz) nz[j] = *row_at(pz, r, ldz);
+            }
+        }
+    };
     fetch(0);
+    for (int i = tid; i < nrows * NG; i += 256) {
+        const int r = i / NG, c = (i % NG) * 4;
+        if (s_slot[r] < 0) continue;
+        sB[i] = quad_f4<E>(ld_vec<E, 4>(static_cast<const E*>(a.Bm) + (row0 + r) * a.ldb + c));
+        sC[i] = quad_f4<E>(ld_vec<E, 4>(static_cast<const E*>(a.Cm) + (row0 + r) * a.ldc + c));
+    }
     const StepRow c = step_consts<ZOH>(l, dsk);
+    float2 finite = f2(0.f);  // becomes NaN with the first infinity or NaN in a state
+    __syncthreads();
     int stage = 0;
     for (int r = 0; r < nrows; r += R) {
-        typename Vec<E, 4>::Raw rB[R], rC[R];
-        E x[R], dr[R], z[R];
+        float dlt[SH], dx[SH], x[SH], z[SH], yp[R];
+        int ky[SH];
 #pragma unroll
-        for (int i = 0; i < R; ++i) { rB[i] = nB[i]; rC[i] = nC[i]; x[i] = nx[i]; dr[i] = nd[i]; z[i] = nz[i]; }
+        for (int j = 0; j < SH; ++j) {
+            ky[j] = nk[j];
+            x[j] = Elem<E>::to_f(nx[j]);
+            z[j] = Elem<E>::to_f(nz[j]);
+            dlt[j] = softplus_fast(Elem<E>::to_f(nd[j]));
+            dx[j] = dlt[j] * x[j];
+        }
         issue(r + (kStepStages - 1) * R, stage == 0 ? kStepStages - 1 : stage - 1);
         fetch(r + R);
         real::cp_async_wait<kStepStages - 1>();
 #pragma unroll
         for (int i = 0; i < R; ++i) {
+            float di = dlt[i % SH], xi = dx[i % SH];
+            if (NG > 1) {
+                di = __shfl_sync(kFull, di, i / SH, NG);
+                xi = __shfl_sync(kFull, xi, i / SH, NG);
+            }
+            yp[i] = 0.f;
             const int k = r + i < nrows ? s_slot[r + i] : -1;
             if (k < 0) continue;  // the whole CTA
-            const float4 h4 = ring[(stage * R + i) * 256];
-            float2 h[2] = {make_float2(h4.x, h4.y), make_float2(h4.z, h4.w)};
-            float v = step_row<E, NG, ZOH>(c, h, x[i], dr[i], rB[i], rC[i]);
-            if (!dv) continue;
-            *reinterpret_cast<float4*>(a.pool + ((size_t)k * a.D + d) * N + n0) =
-                make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
-            if (!real::all_finite<4>(h)) flag_if(a.status, kStatusNonFinite);
-            if (ng == 0) {
-                if (a.z) v *= silu_fast(Elem<E>::to_f(z[i]));
-                static_cast<E*>(a.y)[(size_t)(row0 + r + i) * a.ldy + d] = Elem<E>::from_f(v);
+            const float4 h4 = ring[(stage * R + i) * 256], b4 = sB[(r + i) * NG + ng], c4 = sC[(r + i) * NG + ng];
+            const float2 bq[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
+            const float2 cq[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+            float2 h[2] = {make_float2(h4.x, h4.y), make_float2(h4.z, h4.w)}, acc = f2(0.f);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const float2 e = ex2_pair(__fmul2_rn(f2(di), c.A2[p]));
+                h[p] = __ffma2_rn(e, h[p], input_term<ZOH>(f2(di), f2(xi), e, c.A2[p], c.Ar[p], bq[p]));
+                acc = __ffma2_rn(cq[p], h[p], acc);
+                finite = __ffma2_rn(h[p], f2(0.f), finite);
             }
+            yp[i] = acc.x + acc.y;
+            if (dv) *reinterpret_cast<float4*>(row_at(pool, k, entry)) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+        }
+        real::reduce_scatter<R, NG>(yp, ng);
+#pragma unroll
+        for (int j = 0; j < SH; ++j) {
+            float v = fmaf(c.dsk, x[j], yp[j]);
+            if (pz) v *= silu_fast(z[j]);
+            if (dv && ky[j] >= 0) *row_at(py, r + ng * SH + j, ldy) = Elem<E>::from_f(v);
         }
         stage = stage == kStepStages - 1 ? 0 : stage + 1;
     }
+    if (dv && !(finite.x + finite.y == 0.f)) flag_if(a.status, kStatusNonFinite);
 }
 
 template <typename E, int N, bool ZOH, int FORM>
@@ -534,7 +580,7 @@ cudaError_t step_impl(const ScanServeArgs& a, cudaStream_t st) {
         const int64_t groups = tiles < 296 ? 296 / tiles : 1;
         int64_t rows = ((a.rows + groups - 1) / groups + kStepGroup - 1) / kStepGroup * kStepGroup;
         if (rows > kStepRows) rows = kStepRows;
-        const int smem = kStepStages * kStepGroup * 256 * 16;
+        const int smem = StepCfg<N>::kBytes;
         const cudaError_t e = cudaFuncSetAttribute(scan_step_batch_kernel<E, N, ZOH>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;

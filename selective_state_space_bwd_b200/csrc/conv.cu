@@ -600,38 +600,53 @@ __global__ void __launch_bounds__(kThreads, 2) conv_prompt_kernel(ConvServeArgs 
 }
 
 // ---------------------------------------------------------------- single tokens
-// One row a CTA row: four channels a thread, every load issued before the first use.
-template <typename E, int W, bool SILU>
+// Four channels a thread and R rows a CTA: the taps, as many bytes as a row's state and input in bf16, are read
+// once for the R rows, whose states are on their way together.
+template <typename E, int W, bool SILU, int R>
 __global__ void __launch_bounds__(256) conv_step_kernel(ConvServeArgs a) {
-    const int row = blockIdx.y, c = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
-    const int k = a.slot ? a.slot[row] : row;
-    const bool use = k >= 0 && k < a.slots;
-    const bool work = use && c < a.D;
-    E* entry = static_cast<E*>(a.pool) + (size_t)(use ? k : 0) * (W - 1) * a.D + c;
-    typename Vec<E, 4>::Raw raw[W];
+    using Raw = typename Vec<E, 4>::Raw;
+    const int row0 = blockIdx.y * R, c = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
+    const bool cv = c < a.D;
+    int k[R];
 #pragma unroll
-    for (int j = 0; j < W; ++j) raw[j] = Vec<E, 4>::zero();
-    if (work) {
+    for (int r = 0; r < R; ++r) k[r] = row0 + r < a.rows ? (a.slot ? a.slot[row0 + r] : row0 + r) : -1;
+    Raw raw[R][W];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) raw[j] = ld_vec<E, 4>(entry + (size_t)j * a.D);
-        raw[W - 1] = ld_vec<E, 4>(static_cast<const E*>(a.x) + (size_t)row * a.ldx + c);
+    for (int r = 0; r < R; ++r) {
+        const bool work = cv && k[r] >= 0 && k[r] < a.slots;
+        const E* entry = static_cast<const E*>(a.pool) + (size_t)(work ? k[r] : 0) * (W - 1) * a.D + c;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) raw[r][j] = work ? ld_vec<E, 4>(entry + (size_t)j * a.D) : Vec<E, 4>::zero();
+        raw[r][W - 1] = work ? ld_vec<E, 4>(static_cast<const E*>(a.x) + (size_t)(row0 + r) * a.ldx + c)
+                             : Vec<E, 4>::zero();
     }
-    const bool repeated = a.slot && __syncthreads_or(named_before(a.slot, row, use ? k : -1, threadIdx.x, blockDim.x));
-    if (k >= a.slots || repeated) {
-        if (threadIdx.x == 0 && blockIdx.x == 0) flag_if(a.status, kStatusInvalid);
-        return;
+    float2 w[W][2], bias[2];
+    load_taps<W, 4>(w, bias, a.w, a.bias, cv ? c : 0);
+    if (a.slot) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool in = k[r] >= 0 && k[r] < a.slots;
+            const bool rep = __syncthreads_or(named_before(a.slot, row0 + r, in ? k[r] : -1, threadIdx.x, blockDim.x));
+            if (rep || k[r] >= a.slots) {
+                if (threadIdx.x == 0 && blockIdx.x == 0) flag_if(a.status, kStatusInvalid);
+                k[r] = -1;
+            }
+        }
     }
-    if (!work) return;
-    float2 w[W][2], bias[2], x[U][2], v[2];
-    load_taps<W, 4>(w, bias, a.w, a.bias, c);
+    if (!cv) return;
 #pragma unroll
-    for (int j = 0; j < W; ++j) Vec<E, 4>::unpack(raw[j], x[U - W + j]);
+    for (int r = 0; r < R; ++r) {
+        if (k[r] < 0) continue;
+        float2 x[U][2], v[2];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-        *reinterpret_cast<typename Vec<E, 4>::Raw*>(entry + (size_t)j * a.D) = raw[j + 1];
-    preact<W, 2>(v, w, bias, x, U - 1);
-    if (SILU) silu<2>(v);
-    st_vec<E, 4>(static_cast<E*>(a.y) + (size_t)row * a.ldy + c, v);
+        for (int j = 0; j < W; ++j) Vec<E, 4>::unpack(raw[r][j], x[U - W + j]);
+        E* entry = static_cast<E*>(a.pool) + (size_t)k[r] * (W - 1) * a.D + c;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) *reinterpret_cast<Raw*>(entry + (size_t)j * a.D) = raw[r][j + 1];
+        preact<W, 2>(v, w, bias, x, U - 1);
+        if (SILU) silu<2>(v);
+        st_vec<E, 4>(static_cast<E*>(a.y) + (size_t)(row0 + r) * a.ldy + c, v);
+    }
 }
 
 // ---------------------------------------------------------------- dispatch
@@ -738,10 +753,16 @@ cudaError_t launch_conv_prompt(ConvServeArgs a, int width, bool silu, int io_bf1
 cudaError_t launch_conv_step(const ConvServeArgs& a, int width, bool silu, int io_bf16, cudaStream_t st) {
     const int nvec = (a.D + 3) / 4;
     const int nt = nvec >= 256 ? 256 : (nvec + 31) / 32 * 32;
-    const dim3 grid((nvec + nt - 1) / nt, a.rows), block(nt);
+    const int tiles = (nvec + nt - 1) / nt;
     return conv::dispatch(width, silu, io_bf16, [&](auto e, auto w, auto s) {
         using E = typename decltype(e)::type;
-        conv::conv_step_kernel<E, decltype(w)::value, decltype(s)::value != 0><<<grid, block, 0, st>>>(a);
+        constexpr int W = decltype(w)::value;
+        constexpr bool SL = decltype(s)::value != 0;
+        // four rows a CTA once there are more rows than two CTAs an SM
+        if ((int64_t)tiles * a.rows > 296)
+            conv::conv_step_kernel<E, W, SL, 4><<<dim3(tiles, (a.rows + 3) / 4), nt, 0, st>>>(a);
+        else
+            conv::conv_step_kernel<E, W, SL, 1><<<dim3(tiles, a.rows), nt, 0, st>>>(a);
         return cudaGetLastError();
     });
 }

@@ -408,7 +408,7 @@ struct StepCfg {
 };
 
 template <typename E, int N, bool ZOH>
-__global__ void __launch_bounds__(256, 2) scan_step_batch_kernel(ScanServeArgs a, int rows_per_cta) {
+__global__ void __launch_bounds__(256, 3) scan_step_batch_kernel(ScanServeArgs a, int rows_per_cta) {
     constexpr int NG = N / 4, DC = 256 / NG, R = kStepGroup, SH = R / NG;
     extern __shared__ __align__(16) unsigned char smem[];
     float4* ring = reinterpret_cast<float4*>(smem) + threadIdx.x;  // slot i: ring[i * 256]
@@ -568,7 +568,7 @@ cudaError_t prompt_dispatch(const ScanServeArgs& a, int N, cudaStream_t st) {
     return prompt_pick<E, 16>(a, st);
 }
 
-// One row a CTA while those CTAs run at once (8 an SM); else as many rows a CTA as leave one wave of two
+// One row a CTA while those CTAs run at once (8 an SM); else as many rows a CTA as leave one wave of three
 // CTAs an SM, in whole groups, at most kStepRows.
 template <typename E, int N, bool ZOH>
 cudaError_t step_impl(const ScanServeArgs& a, cudaStream_t st) {
@@ -577,7 +577,7 @@ cudaError_t step_impl(const ScanServeArgs& a, cudaStream_t st) {
     if (tiles * a.rows <= 1184) {
         scan_step_kernel<E, N, ZOH><<<dim3((unsigned)tiles, a.rows), 256, 0, st>>>(a);
     } else {
-        const int64_t groups = tiles < 296 ? 296 / tiles : 1;
+        const int64_t groups = tiles < 444 ? 444 / tiles : 1;
         int64_t rows = ((a.rows + groups - 1) / groups + kStepGroup - 1) / kStepGroup * kStepGroup;
         if (rows > kStepRows) rows = kStepRows;
         const int smem = StepCfg<N>::kBytes;

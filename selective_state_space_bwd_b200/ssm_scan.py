@@ -574,9 +574,9 @@ def _ptr0(t):
 
 def _expect(t, what, shape, dtype, device):
     """A contiguous tensor of this shape, type and device (or None)."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
         return
-    if t.device != device or not t.is_cuda:
+    if t.device != device:
         raise ValueError(f"{what} must be on {device}, is on {t.device}")
     if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
@@ -588,7 +588,7 @@ def _expect_rows(t, what, shape, dtype, device):
     one row stride apart.  Returns the stride in elements (0: dense)."""
     if t is None:
         return 0
-    if t.device != device or not t.is_cuda:
+    if t.device != device:
         raise ValueError(f"{what} must be on {device}, is on {t.device}")
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)}, "
@@ -651,8 +651,14 @@ class _Nothing:
 _HERE_ALREADY = _Nothing()
 
 
+# The current stream's handle: the call that makes no stream object where torch has it (2 us less).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _current(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
 
 
 def _conv_params(w, bias, dim, device):
@@ -672,12 +678,12 @@ def _ws_args(ws, device):
 
 
 def conv_workspace_bytes(shape: SsmConvShape) -> int:
-    return int(lib().ssm_conv_workspace_bytes(ctypes.byref(shape)))
+    return lib().ssm_conv_workspace_bytes(shape)
 
 
 def conv_shape(batch, seqlen, dim, width, io=SSM_BF16, silu=True, ldx=0, ldy=0, lddy=0, lddx=0):
-    return SsmConvShape(int(batch), int(seqlen), int(dim), int(ldx), int(ldy), int(lddy), int(lddx),
-                        int(width), int(io), SSM_CONV_SILU if silu else 0, 0)
+    return SsmConvShape(batch, seqlen, dim, ldx, ldy, lddy, lddx, width, io,
+                        SSM_CONV_SILU if silu else 0, 0)
 
 
 def _q8_expect(q8, shape, device):
@@ -715,7 +721,7 @@ def ssm_conv_fwd(x, w, bias=None, silu=True, s0=None, want_sL=False, want_q8=Fal
         _expect(sL, "sL", (B, W - 1, D), x.dtype, dev)
         q, qe = _q8_expect(q8, x.shape, dev) if q8 is not None else (None, None)
         shape = conv_shape(B, L, D, W, io, silu, ldx, ldy)
-        code = lib().ssm_conv_fwd(shape, x.data_ptr(), w.data_ptr(), _ptr0(bias), _ptr0(s0),
+        code = (_lib or lib()).ssm_conv_fwd(shape, x.data_ptr(), w.data_ptr(), _ptr0(bias), _ptr0(s0),
                                   y.data_ptr(), _ptr0(sL), _ptr0(q), _ptr0(qe), _current(dev))
     _check(code, "ssm_conv_fwd")
     return y, sL, q8
@@ -737,7 +743,7 @@ def ssm_conv_restore(q8, w, bias=None, silu=True, s0=None, dtype=torch.bfloat16,
             y = torch.empty((B, L, D), dtype=dtype, device=dev)
         ldy = _expect_rows(y, "y", q.shape, dtype, dev)
         shape = conv_shape(B, L, D, W, _io_of(y), silu, 0, ldy)
-        code = lib().ssm_conv_restore(shape, q.data_ptr(), qe.data_ptr(), w.data_ptr(), _ptr0(bias),
+        code = (_lib or lib()).ssm_conv_restore(shape, q.data_ptr(), qe.data_ptr(), w.data_ptr(), _ptr0(bias),
                                       _ptr0(s0), y.data_ptr(), _current(dev))
     _check(code, "ssm_conv_restore")
     return y
@@ -778,7 +784,7 @@ def ssm_conv_bwd(x, w, bias, dy, silu=True, s0=None, dsL=None, q8=None, want_ds0
         if ws is None:
             ws = _workspace(conv_workspace_bytes(shape), dev, None)
         wp, wn = _ws_args(ws, dev)
-        code = lib().ssm_conv_bwd(shape, _ptr0(x), _ptr0(q), _ptr0(qe), w.data_ptr(), _ptr0(bias),
+        code = (_lib or lib()).ssm_conv_bwd(shape, _ptr0(x), _ptr0(q), _ptr0(qe), w.data_ptr(), _ptr0(bias),
                                   _ptr0(s0), dy.data_ptr(), _ptr0(dsL), out["dx"].data_ptr(),
                                   out["dw"].data_ptr(), _ptr0(out["dbias"]), _ptr0(out["ds0"]), wp, wn,
                                   _current(dev))
@@ -824,11 +830,11 @@ def _conv_serve(name, x, w, bias, offsets, slots, pool, carry, silu, y, ws, stre
         shape = SsmConvServe(rows, seqs, D, pool.shape[0], ldx, ldy, W, io,
                              SSM_CONV_SILU if silu else 0, 0)
         if offsets is not None:
-            code = lib().ssm_conv_prompt(shape, x.data_ptr(), w.data_ptr(), _ptr0(bias),
+            code = (_lib or lib()).ssm_conv_prompt(shape, x.data_ptr(), w.data_ptr(), _ptr0(bias),
                                          offsets.data_ptr(), slots.data_ptr(), cp, pool.data_ptr(),
                                          y.data_ptr(), wp, wn, _current(dev))
         else:
-            code = lib().ssm_conv_step(shape, x.data_ptr(), w.data_ptr(), _ptr0(bias), _ptr0(slots),
+            code = (_lib or lib()).ssm_conv_step(shape, x.data_ptr(), w.data_ptr(), _ptr0(bias), _ptr0(slots),
                                        pool.data_ptr(), y.data_ptr(), wp, wn, _current(dev))
     _check(code, name)
     return y
@@ -882,12 +888,12 @@ def _scan_serve(name, x, delta_raw, A_log, Bm, Cm, Dskip, offsets, slots, pool, 
         shape = SsmScanServe(rows, seqs, D, N, pool.shape[0], int(max_len), ldx, ldd, ldz, ldb, ldc,
                              ldy, io, SSM_ZOH if zoh else SSM_EULER)
         if offsets is not None:
-            code = lib().ssm_scan_prompt(shape, x.data_ptr(), delta_raw.data_ptr(), A_log.data_ptr(),
+            code = (_lib or lib()).ssm_scan_prompt(shape, x.data_ptr(), delta_raw.data_ptr(), A_log.data_ptr(),
                                          Bm.data_ptr(), Cm.data_ptr(), Dskip.data_ptr(), _ptr0(z),
                                          offsets.data_ptr(), slots.data_ptr(), cp, pool.data_ptr(),
                                          y.data_ptr(), wp, wn, _current(dev))
         else:
-            code = lib().ssm_scan_step(shape, x.data_ptr(), delta_raw.data_ptr(), A_log.data_ptr(),
+            code = (_lib or lib()).ssm_scan_step(shape, x.data_ptr(), delta_raw.data_ptr(), A_log.data_ptr(),
                                        Bm.data_ptr(), Cm.data_ptr(), Dskip.data_ptr(), _ptr0(z),
                                        _ptr0(slots), pool.data_ptr(), y.data_ptr(), wp, wn,
                                        _current(dev))

@@ -482,7 +482,8 @@ int ssm_conv_bwd(const ssm_conv_shape* shape, const void* x, const int8_t* q, co
  * slot are out of range, one longer than max_len, and each that names an entry which an earlier one of
  * the same call names too is left out (its rows of y and its entry stay as they are), and
  * SSM_ERR_INVALID_ARG is recorded in the status word.  SSM_ERR_NONFINITE is recorded as for the
- * other scans.  ws may be NULL (ws_bytes 0) where a call needs only the status word (256 bytes): then
+ * other scans.  (Offsets that run backwards can also make the rows of two sequences overlap; then it is
+ * not determined which of the two wrote them.)  ws may be NULL (ws_bytes 0) where a call needs only the status word (256 bytes): then
  * nothing is recorded, and the call is one kernel with no memset before it.
  *
  * Row strides in elements, 0 = dense; from the row's length to 2^29; of x, y, delta_raw and z a multiple
@@ -491,8 +492,9 @@ int ssm_conv_bwd(const ssm_conv_shape* shape, const void* x, const int8_t* q, co
  * aligned to 4 bytes.  Outputs must not overlap inputs.
  */
 typedef struct ssm_conv_serve {
-    int64_t rows;   /* rows of x and y, 0..2^30 (single tokens: the batch, at most 65535) */
-    int64_t seqs;   /* S, 0..65535 (single tokens: must be 0) */
+    int64_t rows;   /* rows of x and y, 0..2^30 (single tokens: the batch, at most 65535, with slot given
+                       at most 4096: every row is compared with the rows before it) */
+    int64_t seqs;   /* S, 0..4096 (single tokens: must be 0) */
     int64_t dim;    /* D as above */
     int64_t slots;  /* entries of the pool, 0..2^30 */
     int64_t ldx, ldy;

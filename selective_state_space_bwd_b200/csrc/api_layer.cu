@@ -59,13 +59,12 @@ size_t conv_part_bytes(const ssm::ConvArgs& a, int width) {
 int launch_status(cudaError_t e) { return e == cudaSuccess ? SSM_OK : SSM_ERR_CUDA; }
 
 // The status word of a call whose workspace may be absent: *status is null without one.
-int reset_status(void* ws, size_t ws_bytes, size_t need, cudaStream_t s, unsigned** status) {
+int find_status(void* ws, size_t ws_bytes, unsigned** status) {
     *status = nullptr;
-    if (!ws) return need > kStatusBytes || ws_bytes ? SSM_ERR_INVALID_ARG : SSM_OK;
+    if (!ws) return ws_bytes ? SSM_ERR_INVALID_ARG : SSM_OK;
     if (!aligned16(ws)) return SSM_ERR_MISALIGNED;
-    if (ws_bytes < need) return SSM_ERR_WORKSPACE_TOO_SMALL;
+    if (ws_bytes < kStatusBytes) return SSM_ERR_WORKSPACE_TOO_SMALL;
     *status = at<unsigned>(ws, 0);
-    (void)s;
     return SSM_OK;
 }
 
@@ -81,10 +80,14 @@ int check_index(const int32_t* offsets, const int32_t* slot, bool prompts) {
     return SSM_OK;
 }
 
+// Sequences or rows that may name pool entries: each is compared with all before it by every CTA that
+// works on it (4096: half a gigabyte of cached loads in all for 4096 single tokens of 4096 channels).
+constexpr int64_t kMaxNamed = 4096;
+
 int check_rows(int64_t rows, int64_t seqs, int64_t slots, bool prompts) {
     if (rows < 0 || seqs < 0 || slots < 0) return SSM_ERR_INVALID_ARG;
     if (!prompts && seqs != 0) return SSM_ERR_INVALID_ARG;
-    if (rows > (int64_t)1 << 30 || seqs > 65535 || slots > (int64_t)1 << 30) return SSM_ERR_UNSUPPORTED;
+    if (rows > (int64_t)1 << 30 || seqs > kMaxNamed || slots > (int64_t)1 << 30) return SSM_ERR_UNSUPPORTED;
     if (!prompts && rows > 65535) return SSM_ERR_UNSUPPORTED;
     return SSM_OK;
 }
@@ -115,9 +118,10 @@ int conv_serve(const ssm_conv_serve* s, bool prompts, const void* x, const float
     const bool work = prompts ? s->seqs > 0 : rows > 0;
     if (work && (st = check_index(offsets, slot, prompts)) != SSM_OK) return st;
     if (!prompts && !slot && s->rows > s->slots) return SSM_ERR_INVALID_ARG;
+    if (!prompts && slot && s->rows > kMaxNamed) return SSM_ERR_UNSUPPORTED;
     ssm::ConvServeArgs a = {};
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if ((st = reset_status(ws, ws_bytes, kStatusBytes, cs, &a.status)) != SSM_OK) return st;
+    if ((st = find_status(ws, ws_bytes, &a.status)) != SSM_OK) return st;
     if ((st = clear_status(a.status, cs)) != SSM_OK || !work) return st;
     a.rows = (int)rows; a.S = (int)s->seqs; a.D = (int)D; a.slots = (int)s->slots;
     a.ldx = stride(s->ldx, s->dim); a.ldy = stride(s->ldy, s->dim);
@@ -164,9 +168,10 @@ int scan_serve(const ssm_scan_serve* s, bool prompts, const void* x, const void*
     const bool work = prompts ? s->seqs > 0 : rows > 0;
     if (work && (st = check_index(offsets, slot, prompts)) != SSM_OK) return st;
     if (!prompts && !slot && s->rows > s->slots) return SSM_ERR_INVALID_ARG;
+    if (!prompts && slot && s->rows > kMaxNamed) return SSM_ERR_UNSUPPORTED;
     ssm::ScanServeArgs a = {};
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if ((st = reset_status(ws, ws_bytes, kStatusBytes, cs, &a.status)) != SSM_OK) return st;
+    if ((st = find_status(ws, ws_bytes, &a.status)) != SSM_OK) return st;
     if ((st = clear_status(a.status, cs)) != SSM_OK || !work) return st;
     a.rows = (int)rows; a.S = (int)s->seqs; a.D = (int)D; a.slots = (int)s->slots;
     a.max_len = s->max_len && s->max_len < s->rows ? (int)s->max_len : (int)rows;

@@ -669,9 +669,11 @@ cudaError_t dispatch(int width, bool silu, int io_bf16, F f) {
 // Rows a piece of one batch entry: as many as give one wave of CTAs, at least 8 (the W-1 rows before a
 // piece are read twice) and at most 512 (the gradient adds a piece's rows one after another in fp32;
 // its sums over pieces are pairwise or short).  A multiple of four: a word of step exponents.
-int rows_per_piece(int64_t batch, int64_t rows, const Tile& t) {
+// `extra` pieces of the wave are kept free (a packed batch has up to one partly empty piece a sequence).
+int rows_per_piece(int64_t batch, int64_t rows, const Tile& t, int64_t extra) {
     if (batch < 1) batch = 1;
-    const int64_t room = (int64_t)(kResident / t.nct) * t.ry;  // pieces of one channel tile in a wave
+    int64_t room = (int64_t)(kResident / t.nct) * t.ry;  // pieces of one channel tile in a wave
+    if (extra) room = room > 2 * extra ? room - extra : room / 2;
     int64_t n = room / batch;
     if (n < 4) n = 4 * room / batch;  // too few per entry to fill a wave evenly: shorter pieces, more waves
     if (n < 1) n = 1;
@@ -697,7 +699,7 @@ template <typename E> constexpr int kV = 16 / (int)sizeof(E);
 void conv_plan(ConvArgs& a, int io_bf16, bool backward) {
     const conv::Tile t = conv::tile_of(a.D, backward || !io_bf16 ? 4 : 8);
     a.cx = t.cx; a.ry = t.ry; a.nct = t.nct;
-    a.G = conv::rows_per_piece(a.B, a.L, t);
+    a.G = conv::rows_per_piece(a.B, a.L, t, 0);
     a.nseg = a.L > 0 ? (a.L + a.G - 1) / a.G : 1;
     a.parts = (int)(((int64_t)a.B * a.nseg + t.ry - 1) / t.ry);
     a.Lq = ((size_t)a.L + 3) / 4 * 4;
@@ -739,7 +741,7 @@ cudaError_t launch_conv_prompt(ConvServeArgs a, int width, bool silu, int io_bf1
     using namespace conv;
     const Tile t = tile_of(a.D, io_bf16 ? 8 : 4);
     a.cx = t.cx; a.ry = t.ry;
-    a.G = rows_per_piece(1, a.rows, t);
+    a.G = rows_per_piece(1, a.rows, t, a.S);
     a.items = (int64_t)(a.rows / a.G) + a.S;
     const dim3 grid((unsigned)((a.items + t.ry - 1) / t.ry), t.nct);
     return dispatch(width, silu, io_bf16, [&](auto e, auto w, auto s) {

@@ -548,8 +548,10 @@ template <typename E, int N, bool ZOH>
 cudaError_t prompt_impl(ScanServeArgs a, cudaStream_t st) {
     a.ndt = (a.D + PromptCfg<N, kMany>::CW - 1) / PromptCfg<N, kMany>::CW;
     const int64_t ctas = (int64_t)a.S * a.ndt;
-    // worth it when there are more CTAs than run at once, and few enough sequences to be ranked by every CTA
-    a.sorted = a.S > 1 && a.S <= 64 && ctas > 592 && (int64_t)a.max_len * a.S > 2 * (int64_t)a.rows;
+    // Worth it when there are more CTAs than run at once, few enough sequences to be ranked by every CTA, and
+    // a longest one (36 cycles a step) that outweighs the ranking, 2 us a CTA.
+    a.sorted = a.S > 1 && a.S <= 64 && ctas > 592 && a.max_len >= 512 &&
+               (int64_t)a.max_len * a.S > 2 * (int64_t)a.rows;
     if (ctas <= 148) return prompt_launch<E, N, ZOH, kAlone>(a, (unsigned)ctas, st);
     if ((int64_t)a.rows * a.ndt < (int64_t)363 * a.max_len)
         return prompt_launch<E, N, ZOH, kFew>(a, (unsigned)ctas, st);

@@ -182,6 +182,9 @@ def test_serving_pointers_refused(S):
     assert L.ssm_scan_step(s, *[P] * 6, None, P, P, 2 * P, 3 * P, 255, None) == 4
     assert L.ssm_scan_step(s, *[P] * 6, None, P, P, 2 * P, None, 256, None) == 1
     assert L.ssm_scan_step(scan_serve(S, seqs=0, max_len=3), *[P] * 6, None, P, P, 2 * P, None, 0, None) == 1
+    assert L.ssm_scan_step(scan_serve(S, seqs=0, rows=4097, slots=9999), *[P] * 6, None, P, P, 2 * P, None, 0, None) == 2
+    assert L.ssm_conv_step(conv_serve(S, seqs=0, rows=4097), P, P, P, P, P, 2 * P, None, 0, None) == 2
+    assert L.ssm_scan_prompt(scan_serve(S, seqs=4097), *base, None) == 2
     assert L.ssm_scan_step(scan_serve(S, seqs=0, rows=65536), *[P] * 6, None, P, P, 2 * P, None, 0, None) == 2
     s = conv_serve(S, seqs=0)
     assert L.ssm_conv_step(s, P, P, P, None, P, 2 * P, None, 0, None) == 1

@@ -1,15 +1,18 @@
-"""Build libssm_scan.so (all CUDA sources under csrc/) for sm_100a with nvcc, in-tree."""
+"""Build libssm_scan.so (all CUDA sources under csrc/) for sm_100a with nvcc, and the compiled binding
+_ssm_torch.so (csrc/binding.cpp) with the host compiler, in-tree."""
 
 from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libssm_scan.so")
+BINDING = os.path.join(HERE, "_ssm_torch.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -22,16 +25,38 @@ def deps():
         os.path.join(ROOT, "include", "ssm_scan.h")]
 
 
+def binding_deps():
+    return [os.path.join(HERE, "csrc", "binding.cpp"), os.path.join(ROOT, "include", "ssm_scan.h")]
+
+
+def _newer(out, ins) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in ins)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in deps())
+    return _newer(LIB, deps()) and _newer(BINDING, binding_deps())
+
+
+def _binding_commands(obj):
+    """The host compiler's commands for the binding (compile, link), against the installed torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ext
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(os.environ.get("NVCC", "nvcc")))))
+    inc = [sysconfig.get_paths()["include"], *ext.include_paths(), os.path.join(cuda, "include")]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cxx = os.environ.get("CXX", "g++")
+    return ([cxx, "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             "-DTORCH_EXTENSION_NAME=_ssm_torch", *[f"-isystem{p}" for p in inc], "-c", binding_deps()[0], "-o", obj],
+            [cxx, "-shared", obj, "-o", BINDING + ".tmp", f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+             "-lc10", "-lc10_cuda", "-L" + HERE, "-l:libssm_scan.so", "-Wl,-rpath,$ORIGIN"])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every source whose object is stale to an object, in parallel (one nvcc process
-    each; no device code crosses files), then link the shared library."""
+    each; no device code crosses files), then link the shared library and, against it, the binding."""
     if not force and up_to_date():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
@@ -50,11 +75,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     procs = [subprocess.Popen([nvcc, *flags, "-c", src, "-o", obj])
              for src, obj in zip(sources(), objs) if stale(src, obj)]
+    link = None
+    if force or not _newer(BINDING, binding_deps()):
+        compile_, link = _binding_commands(os.path.join(obj_dir, "binding.o"))
+        procs.append(subprocess.Popen(compile_))
     failed = [p.args for p in procs if p.wait() != 0]
     if failed:
         raise subprocess.CalledProcessError(1, failed[0])
-    subprocess.run([nvcc, *ARCH, "-shared", "-o", LIB + ".tmp", *objs], check=True)
-    os.replace(LIB + ".tmp", LIB)
+    if force or not _newer(LIB, [*deps(), *objs]):
+        subprocess.run([nvcc, *ARCH, "-shared", "-Xlinker", "-soname=libssm_scan.so", "-o", LIB + ".tmp", *objs],
+                       check=True)
+        os.replace(LIB + ".tmp", LIB)
+    if link:
+        subprocess.run(link, check=True)
+        os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 

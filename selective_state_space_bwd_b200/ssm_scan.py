@@ -568,133 +568,46 @@ def ssm_dtproj_bwd(u, w, g, want_dbias=True, out=None, ws=None, stream=None):
 # ---------------------------------------------------------------- convolution and serving calls
 
 
-def _ptr0(t):
-    return t.data_ptr() if t is not None else None
+_torch_binding = None
 
 
-def _expect(t, what, shape, dtype, device):
-    """A contiguous tensor of this shape, type and device (or None)."""
-    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
-        return
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, is on {t.device}")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"is {t.dtype} {tuple(t.shape)}")
-
-
-def _expect_rows(t, what, shape, dtype, device):
-    """A tensor of rows that may be strided: [..., D] with dense columns, its leading dimensions
-    one row stride apart.  Returns the stride in elements (0: dense)."""
-    if t is None:
-        return 0
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, is on {t.device}")
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)}, "
-                         f"is {t.dtype} {tuple(t.shape)}")
-    if t.is_contiguous():
-        return 0
-    ld, rows = 0, 1
-    strides = t.stride()
-    for size, st in zip(reversed(shape[:-1]), reversed(strides[:-1])):
-        if size > 1:
-            if rows > 1 and st != ld * rows:
-                raise ValueError(f"{what}: rows must lie one stride apart, strides are {strides}")
-            if rows == 1:
-                ld = st
-            rows *= size
-    if strides[-1] != 1 or (rows > 1 and ld < shape[-1]):
-        raise ValueError(f"{what}: columns must be dense and rows must not overlap, strides are {strides}")
-    return ld
-
-
-def _io_tensor(t, what, ndim):
-    if not isinstance(t, torch.Tensor) or t.dim() != ndim or not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor of {ndim} dimensions")
-    return t.device, _io_of(t)
+def _native():
+    """The compiled binding of these calls, _ssm_torch.so (opened once).  Raises if it has not been built."""
+    global _torch_binding
+    if _torch_binding is None:
+        if not os.path.exists(os.path.join(_HERE, "_ssm_torch.so")):
+            raise RuntimeError(f"{_HERE}/_ssm_torch.so is missing: build it with "
+                               "`python -m selective_state_space_bwd_b200.build` (no CPU fallback)")
+        lib()
+        from . import _ssm_torch as b
+        b.set_error_class(SsmError)
+        _torch_binding = b
+    return _torch_binding
 
 
 class _On:
-    """Makes the tensors' device and the launch stream current for a call and its allocations, so
-    that a workspace allocated here is only handed out again in that stream's order."""
+    """Makes a given launch stream, and its device, current for a call and its allocations, so that a workspace
+    allocated here is only handed out again in that stream's order."""
 
-    def __new__(cls, device, stream):
-        if stream is None and torch.cuda.current_device() == device.index:
-            return _HERE_ALREADY
-        return super().__new__(cls)
-
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        self.guards = [torch.cuda.device(device)]
-        if stream is not None:
-            self.guards.append(torch.cuda.stream(stream))
+    def __init__(self, t, stream):
+        if stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+        self.guard = torch.cuda.stream(stream)
 
     def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
+        self.guard.__enter__()
 
     def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
-
-
-class _Nothing:
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
-
-
-_HERE_ALREADY = _Nothing()
-
-
-# The current stream's handle: the call that makes no stream object where torch has it (2 us less).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _current(device):
-    if _raw_stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return _raw_stream(device.index)
-
-
-def _conv_params(w, bias, dim, device):
-    if w.dim() != 2:
-        raise ValueError("w must be [D, W]")
-    _expect(w, "w", (dim, w.shape[1]), torch.float32, device)
-    _expect(bias, "bias", (dim,), torch.float32, device)
-    return w.shape[1]
-
-
-def _ws_args(ws, device):
-    if ws is None:
-        return None, 0
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous tensor on {device}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+        self.guard.__exit__(*exc)
 
 
 def conv_workspace_bytes(shape: SsmConvShape) -> int:
-    return lib().ssm_conv_workspace_bytes(shape)
+    return int(lib().ssm_conv_workspace_bytes(ctypes.byref(shape)))
 
 
 def conv_shape(batch, seqlen, dim, width, io=SSM_BF16, silu=True, ldx=0, ldy=0, lddy=0, lddx=0):
-    return SsmConvShape(batch, seqlen, dim, ldx, ldy, lddy, lddx, width, io,
-                        SSM_CONV_SILU if silu else 0, 0)
-
-
-def _q8_expect(q8, shape, device):
-    q, qe = q8
-    _expect(q, "q", shape, torch.int8, device)
-    _expect(qe, "qe", _qe_shape(*shape), torch.uint8, device)
-    return q, qe
-
-
-def _qe_shape(B, L, D):
-    return B, -(-D // 32), -(-L // 4) * 4
+    return SsmConvShape(int(batch), int(seqlen), int(dim), int(ldx), int(ldy), int(lddy), int(lddx),
+                        int(width), int(io), SSM_CONV_SILU if silu else 0, 0)
 
 
 def ssm_conv_fwd(x, w, bias=None, silu=True, s0=None, want_sL=False, want_q8=False, y=None, sL=None,
@@ -702,142 +615,42 @@ def ssm_conv_fwd(x, w, bias=None, silu=True, s0=None, want_sL=False, want_q8=Fal
     """Short causal convolution y = [SiLU](bias + sum_j w[:, j] x_{t-(W-1)+j}).  x [B,L,D] fp32 or
     bf16, rows may be strided; w [D,W] (W = 2..4), bias [D] fp32; s0 [B,W-1,D] the inputs before
     step 0 (None: zero).  Returns (y [B,L,D], sL, q8): sL [B,W-1,D] the last inputs (if ``want_sL`` or
-    ``sL`` is given, else None), q8 = (q [B,L,D] int8, qe [B, ceil(D/32), L rounded up to 4] uint8) the 8-bit
-    checkpoint of x (if ``want_q8`` or ``q8`` is given, else None)."""
-    dev, io = _io_tensor(x, "x", 3)
-    B, L, D = x.shape
-    ldx = _expect_rows(x, "x", x.shape, x.dtype, dev)
-    W = _conv_params(w, bias, D, dev)
-    _expect(s0, "s0", (B, W - 1, D), x.dtype, dev)
-    with _On(dev, stream):
-        if y is None:
-            y = torch.empty((B, L, D), dtype=x.dtype, device=dev)
-        if sL is None and want_sL:
-            sL = torch.empty((B, W - 1, D), dtype=x.dtype, device=dev)
-        if q8 is None and want_q8:
-            q8 = (torch.empty((B, L, D), dtype=torch.int8, device=dev),
-                  torch.empty(_qe_shape(B, L, D), dtype=torch.uint8, device=dev))
-        ldy = _expect_rows(y, "y", x.shape, x.dtype, dev)
-        _expect(sL, "sL", (B, W - 1, D), x.dtype, dev)
-        q, qe = _q8_expect(q8, x.shape, dev) if q8 is not None else (None, None)
-        shape = conv_shape(B, L, D, W, io, silu, ldx, ldy)
-        code = (_lib or lib()).ssm_conv_fwd(shape, x.data_ptr(), w.data_ptr(), _ptr0(bias), _ptr0(s0),
-                                  y.data_ptr(), _ptr0(sL), _ptr0(q), _ptr0(qe), _current(dev))
-    _check(code, "ssm_conv_fwd")
-    return y, sL, q8
+    ``sL`` is given, else None), q8 = (q [B,L,D] int8, qe [B, ceil(D/32), L rounded up to 4] uint8) the
+    8-bit checkpoint of x (if ``want_q8`` or ``q8`` is given, else None)."""
+    if stream is not None:
+        with _On(x, stream):
+            return ssm_conv_fwd(x, w, bias, silu, s0, want_sL, want_q8, y, sL, q8)
+    q, qe = q8 if q8 is not None else (None, None)
+    y, sL, q, qe = _native().conv_fwd(x, w, bias, silu, s0, want_sL, want_q8, y, sL, q, qe)
+    return y, sL, None if q is None else (q, qe)
 
 
 def ssm_conv_restore(q8, w, bias=None, silu=True, s0=None, dtype=torch.bfloat16, y=None, stream=None):
     """y of ssm_conv_fwd recomputed from the 8-bit checkpoint (q, qe), in ``dtype`` (the forward's
     io type).  Returns y [B,L,D]."""
-    q, qe = q8
-    if q.dim() != 3:
-        raise ValueError("q must be [B, L, D]")
-    dev = q.device
-    B, L, D = q.shape
-    q, qe = _q8_expect(q8, q.shape, dev)
-    W = _conv_params(w, bias, D, dev)
-    _expect(s0, "s0", (B, W - 1, D), dtype, dev)
-    with _On(dev, stream):
-        if y is None:
-            y = torch.empty((B, L, D), dtype=dtype, device=dev)
-        ldy = _expect_rows(y, "y", q.shape, dtype, dev)
-        shape = conv_shape(B, L, D, W, _io_of(y), silu, 0, ldy)
-        code = (_lib or lib()).ssm_conv_restore(shape, q.data_ptr(), qe.data_ptr(), w.data_ptr(), _ptr0(bias),
-                                      _ptr0(s0), y.data_ptr(), _current(dev))
-    _check(code, "ssm_conv_restore")
-    return y
+    if stream is not None:
+        with _On(q8[0], stream):
+            return ssm_conv_restore(q8, w, bias, silu, s0, dtype, y)
+    return _native().conv_restore(q8[0], q8[1], w, bias, silu, s0, dtype, y)
 
 
 def ssm_conv_bwd(x, w, bias, dy, silu=True, s0=None, dsL=None, q8=None, want_ds0=None, out=None,
                  ws=None, stream=None):
     """Gradient of sum(dy y) + sum(dsL sL) of ssm_conv_fwd, from its input x, or (x None) from the
     8-bit checkpoint q8.  Returns dict dx [B,L,D] io type, dw [D,W] and dbias [D] fp32 (None without a
-    bias), ds0 [B,W-1,D] (if ``want_ds0``; by default with s0 or dsL; else None)."""
-    dev, io = _io_tensor(dy, "dy", 3)
-    B, L, D = dy.shape
-    if (x is None) == (q8 is None):
-        raise ValueError("give either x or q8")
-    ldx = _expect_rows(x, "x", dy.shape, dy.dtype, dev)
-    lddy = _expect_rows(dy, "dy", dy.shape, dy.dtype, dev)
-    q, qe = _q8_expect(q8, dy.shape, dev) if q8 is not None else (None, None)
-    W = _conv_params(w, bias, D, dev)
-    _expect(s0, "s0", (B, W - 1, D), dy.dtype, dev)
-    _expect(dsL, "dsL", (B, W - 1, D), dy.dtype, dev)
+    bias), ds0 [B,W-1,D] (if ``want_ds0``; by default with s0 or dsL; else None).  Arrays given in
+    ``out`` are written in place."""
+    if stream is not None:
+        with _On(dy, stream):
+            return ssm_conv_bwd(x, w, bias, dy, silu, s0, dsL, q8, want_ds0, out, ws)
     if want_ds0 is None:
         want_ds0 = s0 is not None or dsL is not None
-    with _On(dev, stream):
-        out = {} if out is None else out
-        if out.get("dx") is None:
-            out["dx"] = torch.empty((B, L, D), dtype=dy.dtype, device=dev)
-        if out.get("dw") is None:
-            out["dw"] = torch.empty((D, W), dtype=torch.float32, device=dev)
-        if out.get("dbias") is None:
-            out["dbias"] = torch.empty((D,), dtype=torch.float32, device=dev) if bias is not None else None
-        if out.get("ds0") is None:
-            out["ds0"] = torch.empty((B, W - 1, D), dtype=dy.dtype, device=dev) if want_ds0 else None
-        lddx = _expect_rows(out["dx"], "dx", dy.shape, dy.dtype, dev)
-        _expect(out["dw"], "dw", (D, W), torch.float32, dev)
-        _expect(out["dbias"], "dbias", (D,), torch.float32, dev)
-        _expect(out["ds0"], "ds0", (B, W - 1, D), dy.dtype, dev)
-        shape = conv_shape(B, L, D, W, io, silu, ldx, 0, lddy, lddx)
-        if ws is None:
-            ws = _workspace(conv_workspace_bytes(shape), dev, None)
-        wp, wn = _ws_args(ws, dev)
-        code = (_lib or lib()).ssm_conv_bwd(shape, _ptr0(x), _ptr0(q), _ptr0(qe), w.data_ptr(), _ptr0(bias),
-                                  _ptr0(s0), dy.data_ptr(), _ptr0(dsL), out["dx"].data_ptr(),
-                                  out["dw"].data_ptr(), _ptr0(out["dbias"]), _ptr0(out["ds0"]), wp, wn,
-                                  _current(dev))
-    _check(code, "ssm_conv_bwd")
+    q, qe = q8 if q8 is not None else (None, None)
+    out = {} if out is None else out
+    out["dx"], out["dw"], out["dbias"], out["ds0"] = _native().conv_bwd(
+        x, q, qe, w, bias, dy, silu, s0, dsL, want_ds0, out.get("dx"), out.get("dw"), out.get("dbias"),
+        out.get("ds0"), ws)
     return out
-
-
-def _flags8(carry, seqs, device):
-    if carry is None:
-        return None
-    if carry.dtype == torch.bool:
-        carry = carry.view(torch.uint8)
-    _expect(carry, "carry", (seqs,), torch.uint8, device)
-    return carry.data_ptr()
-
-
-def _prompt_index(offsets, slots, device):
-    if offsets.dim() != 1 or offsets.shape[0] < 1:
-        raise ValueError("offsets must hold one int32 a sequence and one more")
-    seqs = offsets.shape[0] - 1
-    _expect(offsets, "offsets", (seqs + 1,), torch.int32, device)
-    _expect(slots, "slots", (seqs,), torch.int32, device)
-    return seqs
-
-
-def _conv_serve(name, x, w, bias, offsets, slots, pool, carry, silu, y, ws, stream):
-    dev, io = _io_tensor(x, "x", 2)
-    rows, D = x.shape
-    ldx = _expect_rows(x, "x", x.shape, x.dtype, dev)
-    W = _conv_params(w, bias, D, dev)
-    _expect(pool, "pool", (pool.shape[0], W - 1, D), x.dtype, dev)
-    if offsets is not None:
-        seqs = _prompt_index(offsets, slots, dev)
-        cp = _flags8(carry, seqs, dev)
-    else:
-        seqs = 0
-        _expect(slots, "slots", (rows,), torch.int32, dev)
-    wp, wn = _ws_args(ws, dev)
-    with _On(dev, stream):
-        if y is None:
-            y = torch.empty((rows, D), dtype=x.dtype, device=dev)
-        ldy = _expect_rows(y, "y", x.shape, x.dtype, dev)
-        shape = SsmConvServe(rows, seqs, D, pool.shape[0], ldx, ldy, W, io,
-                             SSM_CONV_SILU if silu else 0, 0)
-        if offsets is not None:
-            code = (_lib or lib()).ssm_conv_prompt(shape, x.data_ptr(), w.data_ptr(), _ptr0(bias),
-                                         offsets.data_ptr(), slots.data_ptr(), cp, pool.data_ptr(),
-                                         y.data_ptr(), wp, wn, _current(dev))
-        else:
-            code = (_lib or lib()).ssm_conv_step(shape, x.data_ptr(), w.data_ptr(), _ptr0(bias), _ptr0(slots),
-                                       pool.data_ptr(), y.data_ptr(), wp, wn, _current(dev))
-    _check(code, name)
-    return y
 
 
 def ssm_conv_prompt(x, w, bias, offsets, slots, pool, carry=None, silu=True, y=None, ws=None,
@@ -849,56 +662,19 @@ def ssm_conv_prompt(x, w, bias, offsets, slots, pool, carry=None, silu=True, y=N
     written.  ``ws`` (256 bytes, optional) receives the status word.  Returns y [R,D]."""
     if offsets is None:
         raise ValueError("offsets is needed")
-    return _conv_serve("ssm_conv_prompt", x, w, bias, offsets, slots, pool, carry, silu, y, ws, stream)
+    if stream is not None:
+        with _On(x, stream):
+            return ssm_conv_prompt(x, w, bias, offsets, slots, pool, carry, silu, y, ws)
+    return _native().conv_serve(x, w, bias, offsets, slots, pool, carry, silu, y, ws)
 
 
 def ssm_conv_step(x, w, bias, slots, pool, silu=True, y=None, ws=None, stream=None):
     """Convolution of single tokens: row b of x [B,D] continues pool entry slots[b] (int32 on the
     device; None: entry b; negative: a padding row, left alone).  Returns y [B,D]."""
-    return _conv_serve("ssm_conv_step", x, w, bias, None, slots, pool, None, silu, y, ws, stream)
-
-
-def _scan_serve(name, x, delta_raw, A_log, Bm, Cm, Dskip, offsets, slots, pool, carry, z, zoh, max_len,
-                y, ws, stream):
-    dev, io = _io_tensor(x, "x", 2)
-    rows, D = x.shape
-    if A_log.dim() != 2:
-        raise ValueError("A_log must be [D, N]")
-    N, dt = A_log.shape[1], x.dtype
-    bshape = torch.Size((rows, N))
-    ldx = _expect_rows(x, "x", x.shape, dt, dev)
-    ldd = _expect_rows(delta_raw, "delta_raw", x.shape, dt, dev)
-    ldz = _expect_rows(z, "z", x.shape, dt, dev)
-    ldb = _expect_rows(Bm, "Bm", bshape, dt, dev)
-    ldc = _expect_rows(Cm, "Cm", bshape, dt, dev)
-    _expect(A_log, "A_log", (D, N), torch.float32, dev)
-    _expect(Dskip, "Dskip", (D,), torch.float32, dev)
-    _expect(pool, "pool", (pool.shape[0], D, N), torch.float32, dev)
-    if offsets is not None:
-        seqs = _prompt_index(offsets, slots, dev)
-        cp = _flags8(carry, seqs, dev)
-    else:
-        seqs = 0
-        _expect(slots, "slots", (rows,), torch.int32, dev)
-    wp, wn = _ws_args(ws, dev)
-    with _On(dev, stream):
-        if y is None:
-            y = torch.empty((rows, D), dtype=dt, device=dev)
-        ldy = _expect_rows(y, "y", x.shape, dt, dev)
-        shape = SsmScanServe(rows, seqs, D, N, pool.shape[0], int(max_len), ldx, ldd, ldz, ldb, ldc,
-                             ldy, io, SSM_ZOH if zoh else SSM_EULER)
-        if offsets is not None:
-            code = (_lib or lib()).ssm_scan_prompt(shape, x.data_ptr(), delta_raw.data_ptr(), A_log.data_ptr(),
-                                         Bm.data_ptr(), Cm.data_ptr(), Dskip.data_ptr(), _ptr0(z),
-                                         offsets.data_ptr(), slots.data_ptr(), cp, pool.data_ptr(),
-                                         y.data_ptr(), wp, wn, _current(dev))
-        else:
-            code = (_lib or lib()).ssm_scan_step(shape, x.data_ptr(), delta_raw.data_ptr(), A_log.data_ptr(),
-                                       Bm.data_ptr(), Cm.data_ptr(), Dskip.data_ptr(), _ptr0(z),
-                                       _ptr0(slots), pool.data_ptr(), y.data_ptr(), wp, wn,
-                                       _current(dev))
-    _check(code, name)
-    return y
+    if stream is not None:
+        with _On(x, stream):
+            return ssm_conv_step(x, w, bias, slots, pool, silu, y, ws)
+    return _native().conv_serve(x, w, bias, None, slots, pool, None, silu, y, ws)
 
 
 def ssm_scan_prompt(x, delta_raw, A_log, Bm, Cm, Dskip, offsets, slots, pool, carry=None, z=None,
@@ -910,13 +686,19 @@ def ssm_scan_prompt(x, delta_raw, A_log, Bm, Cm, Dskip, offsets, slots, pool, ca
     Returns y [R,D]."""
     if offsets is None:
         raise ValueError("offsets is needed")
-    return _scan_serve("ssm_scan_prompt", x, delta_raw, A_log, Bm, Cm, Dskip, offsets, slots, pool,
-                       carry, z, zoh, max_len, y, ws, stream)
+    if stream is not None:
+        with _On(x, stream):
+            return ssm_scan_prompt(x, delta_raw, A_log, Bm, Cm, Dskip, offsets, slots, pool, carry, z, zoh,
+                                   max_len, y, ws)
+    return _native().scan_serve(x, delta_raw, A_log, Bm, Cm, Dskip, offsets, slots, pool, carry, z, zoh,
+                                max_len, y, ws)
 
 
 def ssm_scan_step(x, delta_raw, A_log, Bm, Cm, Dskip, slots, pool, z=None, zoh=False, y=None, ws=None,
                   stream=None):
     """Scan of single tokens: row b continues pool entry slots[b] (None: entry b; negative: a
     padding row, left alone).  Returns y [B,D]."""
-    return _scan_serve("ssm_scan_step", x, delta_raw, A_log, Bm, Cm, Dskip, None, slots, pool, None,
-                       z, zoh, 0, y, ws, stream)
+    if stream is not None:
+        with _On(x, stream):
+            return ssm_scan_step(x, delta_raw, A_log, Bm, Cm, Dskip, slots, pool, z, zoh, y, ws)
+    return _native().scan_serve(x, delta_raw, A_log, Bm, Cm, Dskip, None, slots, pool, None, z, zoh, 0, y, ws)

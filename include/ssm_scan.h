@@ -486,6 +486,9 @@ int ssm_conv_bwd(const ssm_conv_shape* shape, const void* x, const int8_t* q, co
  * not determined which of the two wrote them.)  ws may be NULL (ws_bytes 0) where a call needs only the status word (256 bytes): then
  * nothing is recorded, and the call is one kernel with no memset before it.
  *
+ * Which kernel runs depends on the batch's sizes: repeats are bitwise equal, and a sequence's results in
+ * different batches, or cut into several calls, agree to rounding (the convolution's are bitwise equal).
+ *
  * Row strides in elements, 0 = dense; from the row's length to 2^29; of x, y, delta_raw and z a multiple
  * of 16 bytes with 16-byte aligned pointers, of Bm and Cm a multiple of 4 elements with pointers aligned
  * to 4 elements: columns of a projection's output are used in place.  offsets and slot are

@@ -12,7 +12,7 @@
 // ahead, computes transitions and input terms of all U steps, then waits for the state from the warp
 // before, runs its U steps, hands the state on through shared memory and a named barrier, and finishes its y's
 // while the others go on.  A sequence of any length is one pass: nothing is evaluated twice, no segment
-// summaries, no workspace, and the result does not depend on a split.  (Measured before: time segments
+// summaries, no workspace, and no split to choose.  (Measured before: time segments
 // with summaries and a carry, which evaluate every exp2 twice: 4096 steps of 1536 channels took 98 us
 // against 86, a ragged batch of 24 prompts on 4096 channels 445 us against 325.)
 //
@@ -27,7 +27,6 @@ namespace {
 using real::ex2_pair;
 using real::f2;
 using real::kFull;
-
 
 // four B or C elements of a row, as fp32
 template <typename E>

@@ -119,6 +119,83 @@ def test_scan_prompt(S, oracle_mod, lens, D, N, gate, zoh, io):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("zoh", [False, True])
+@pytest.mark.parametrize("N,D,kind", [(16, 520, "even"), (8, 520, "even"), (4, 520, "even"), (16, 1544, "uneven")])
+def test_scan_prompt_on_a_full_gpu(S, oracle_mod, N, D, kind, zoh, io):
+    """Batches with many more CTAs than run at once (the form whose SMs are shared), and one of them with
+    lengths uneven enough for the longest sequences to be started first."""
+    g = torch.Generator().manual_seed(N)
+    if kind == "even":
+        lens = (torch.randint(1, 65, (110,), generator=g)).tolist()
+    else:
+        lens = [3, 600, 250] + torch.randint(0, 300, (14,), generator=g).tolist()
+    n = len(lens)
+    slots = [n - 1 - i if i % 5 else -1 for i in range(n)]
+    t = batch(lens, D, N, 4, io, N + D, slots, n)
+    y = torch.full((t["x"].shape[0], D), 7, dtype=DT[io], device="cuda")
+    args = [t[k] for k in ("x", "delta_raw", "A_log", "Bm", "Cm", "Dskip", "offsets", "slots")]
+    pool = t["spool"].clone()
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    S.ssm_scan_prompt(*args, pool, carry=t["carry"], z=t["z"], zoh=zoh, max_len=max(lens), y=y, ws=ws)
+    assert S.ssm_scan_status(ws) == S.SSM_OK
+    ry, rpool = oracle_mod.scan_serve(*[f64(t[k]) for k in ("x", "delta_raw", "A_log", "Bm", "Cm", "Dskip")],
+                                      host(t["offsets"]), slots, f64(t["spool"]), host(t["carry"]), f64(t["z"]),
+                                      zoh, y=7.0)
+    check_prompt(y, pool, ry, rpool, t, io, 1e-5, 1e-5)
+
+
+@pytest.mark.parametrize("n", [300, 1500, 4096])
+def test_prompts_of_many_sequences(S, oracle_mod, n):
+    D, N, W = 24, 4, 3
+    lens = torch.randint(0, 6, (n,), generator=torch.Generator().manual_seed(n)).tolist()
+    slots = torch.randperm(n + 5, generator=torch.Generator().manual_seed(n))[:n].tolist()
+    t = batch(lens, D, N, W, "f32", n, slots, n + 5)
+    off, cry = host(t["offsets"]), host(t["carry"])
+    y = torch.full((t["x"].shape[0], D), 7.0, device="cuda")
+    pool = t["cpool"].clone()
+    S.ssm_conv_prompt(t["x"], t["w"], t["bias"], t["offsets"], t["slots"], pool, carry=t["carry"], y=y)
+    ry, rp = oracle_mod.conv_serve(f64(t["x"]), f64(t["w"]), f64(t["bias"]), off, slots, f64(t["cpool"]), cry, y=7.0)
+    assert np.array_equal(f64(pool), rp) and np.abs(f64(y) - ry).max() <= 4e-6 * np.abs(ry).max()
+    args = [t[k] for k in ("x", "delta_raw", "A_log", "Bm", "Cm", "Dskip")]
+    y = torch.full_like(y, 7.0)
+    pool = t["spool"].clone()
+    S.ssm_scan_prompt(*args, t["offsets"], t["slots"], pool, carry=t["carry"], y=y)
+    ry, rp = oracle_mod.scan_serve(*[f64(a) for a in args], off, slots, f64(t["spool"]), cry, y=7.0)
+    assert np.abs(f64(y) - ry).max() <= 2e-5 * np.abs(ry).max()
+    assert np.abs(f64(pool) - rp).max() <= 2e-5 * np.abs(rp).max()
+
+
+def test_largest_batch_of_single_tokens_that_name_entries(S):
+    """4096 rows, entry 17 named by three of them: the first has it."""
+    B, D, N = 4096, 64, 16
+    slots = torch.randperm(B, generator=torch.Generator().manual_seed(1)).int()
+    at = int((slots == 17).nonzero())
+    for b in (at + 1, B - 1) if at < B - 2 else (at - 2, at - 1):
+        slots[b] = 17
+    first = int((slots == 17).nonzero()[0])
+    t = batch([1] * B, D, N, 4, "bf16", 2, slots.tolist(), B, pad=0)
+    args = [t[k] for k in ("x", "delta_raw", "A_log", "Bm", "Cm", "Dskip")]
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    for name in ("spool", "cpool"):
+        def run(rows, sl, pool, y):
+            if name == "spool":
+                return S.ssm_scan_step(*rows, sl, pool, y=y, ws=ws)
+            return S.ssm_conv_step(rows[0], t["w"], t["bias"], sl, pool, y=y, ws=ws)
+        a, b = t[name].clone(), t[name].clone()
+        y = torch.full((B, D), 7, dtype=torch.bfloat16, device="cuda")
+        run(args, t["slots"], a, y)
+        assert S.ssm_scan_status(ws) == 1
+        good = [i for i in range(B) if slots[i] != 17 or i == first]
+        rows = [x[good] if x.shape[0] == B and x.dim() == 2 and x.shape[1] != N or x is args[3] or x is args[4] else x
+                for x in args]
+        want = run(rows, t["slots"][good].contiguous(), b, torch.empty(len(good), D, dtype=torch.bfloat16, device="cuda"))
+        assert S.ssm_scan_status(ws) == 0
+        assert torch.equal(a, b) and torch.equal(y[good], want)
+        bad = [i for i in range(B) if i not in set(good)]
+        assert len(bad) == 2 and bool((y[bad] == 7).all())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("B,D,W", [(1, 8, 4), (3, 1544, 2), (70, 264, 3), (300, 32, 4), (5, 4096, 4)])
 def test_conv_step(S, oracle_mod, B, D, W, io):
     perm = torch.randperm(B + 4, generator=torch.Generator().manual_seed(B)).int()

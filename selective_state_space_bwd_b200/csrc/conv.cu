@@ -5,8 +5,8 @@
 // in the gradient, the fp32 pipes not far behind.  A thread owns V consecutive
 // channels and walks down a piece of the rows, the last W-1 inputs in registers, so that an element
 // is read once from DRAM (the W-1 rows before a piece a second time).  Each thread copies its
-// own rows into its own places of a ring in shared memory, kDepth groups of four rows ahead
-// (cp.async, 16 or 8 bytes): the bytes in flight, about 64 KB an SM, cost no registers, and since no other
+// own rows into its own places of a ring in shared memory, kDepth - 1 groups of four rows ahead
+// (cp.async, 16 or 8 bytes): the bytes in flight, 32 to 64 KB an SM, cost no registers, and since no other
 // thread reads them there is no barrier in the loop, only the thread's own wait_group.
 //
 // A CTA is cx threads across (a multiple of the 32 / V threads that share an 8-bit group's 32 channels, so
@@ -229,7 +229,9 @@ __device__ __forceinline__ void past_row(float2 (&o)[V / 2], const E* s0, int t,
 template <typename E, int V, int W, bool SILU, bool SRC8, bool DST8>
 struct Fwd {
     using R = Rows<E, V, SRC8>;
-    static constexpr int kDepth = sizeof(typename R::Raw) == 16 ? 3 : 4;
+    // Groups in the ring: one or two on their way.  Bytes in flight are not what the forward waits for: at
+    // 4 x 8192 x 4096 it takes 94 us with one group of 16-byte rows ahead, 103 with two to four.
+    static constexpr int kDepth = sizeof(typename R::Raw) == 16 ? 2 : 3;
     static constexpr int kBytes = kDepth * U * kThreads * (int)sizeof(typename R::Raw);
 };
 

@@ -63,21 +63,21 @@ __device__ __forceinline__ float2 softplus_pair(float2 v) {
 // Prompts.  A lane owns four states of two neighbouring channels: NG = N / 4 lanes a pair of channels, CW
 // channels a CTA.  Each of its NW warps holds all of them, for its turns of U steps.  Row by row a lane
 // holds SH of a turn's steps, the same ones whose sums the reduction over the NG lanes leaves in it.
-// Three forms, chosen by prompt_impl:
-//   kMany: turns of four steps, four warps a CTA, four CTAs an SM, which share it.
-//   kFew: turns of eight steps, eight warps and one CTA an SM: fewer hand-overs a step.
-//   kAlone: as kFew, but what counts is how soon a warp hands the state on, so a turn is first reduced to
-//   h_out = P h_in + S (more arithmetic, but off the chain from warp to warp).
-enum Form { kMany, kFew, kAlone };
-template <int N, int FORM>
+// Two forms, chosen by prompt_impl:
+//   MANY: turns of four steps, four warps a CTA, four CTAs an SM, which share it.
+//   Few: turns of eight steps, eight warps and one CTA an SM, so that a step's share of the hand-over is small.
+//   With N = 16 a turn is also reduced to h_out = P h_in + S before the state arrives (kWhole): more
+//   arithmetic, but only one product on the chain from warp to warp (one sequence of 3000 steps on 4096 channels
+//   145 -> 127 us; with N = 8 the arithmetic costs what the chain gains, with N = 4 more: 92 against 132).
+template <int N, bool MANY>
 struct PromptCfg {
-    static constexpr bool MANY = FORM == kMany;
     static constexpr int NG = N / 4;
     static constexpr int CW = 64 / NG;
     static constexpr int U = MANY ? 4 : 8;
     static constexpr int NW = MANY ? 4 : 8;
     static constexpr int SH = U / NG;
     static constexpr int kCtas = MANY ? 4 : 1;   // an SM
+    static constexpr bool kWhole = !MANY && N == 16;
 };
 
 // A pair of neighbouring channels as it lies in a row.
@@ -97,11 +97,11 @@ template <> struct Pair<__nv_bfloat16> {
 __device__ __forceinline__ void hand_wait(int w) { asm volatile("bar.sync %0, 64;" ::"r"(w + 1) : "memory"); }
 __device__ __forceinline__ void hand_over(int w) { asm volatile("bar.arrive %0, 64;" ::"r"(w + 1) : "memory"); }
 
-template <typename E, int N, bool ZOH, int FORM>
-__global__ void __launch_bounds__(PromptCfg<N, FORM>::NW * 32, PromptCfg<N, FORM>::kCtas)
+template <typename E, int N, bool ZOH, bool MANY>
+__global__ void __launch_bounds__(PromptCfg<N, MANY>::NW * 32, PromptCfg<N, MANY>::kCtas)
 scan_prompt_kernel(ScanServeArgs a) {
-    using Cfg = PromptCfg<N, FORM>;
-    constexpr bool ALONE = FORM == kAlone;
+    using Cfg = PromptCfg<N, MANY>;
+    constexpr bool WHOLE = Cfg::kWhole;
     using PR = typename Pair<E>::Raw;
     using BR = typename Vec<E, 4>::Raw;
     constexpr int NG = Cfg::NG, CW = Cfg::CW, U = Cfg::U, SH = Cfg::SH, NP = CW / 2, NW = Cfg::NW;
@@ -233,7 +233,7 @@ scan_prompt_kernel(ScanServeArgs a) {
             }
         }
         float2 P[2][2], out[2][2];  // the turn as a whole: out = P h + out
-        if (ALONE) {
+        if (WHOLE) {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -267,11 +267,11 @@ scan_prompt_kernel(ScanServeArgs a) {
 #pragma unroll
                     for (int p = 0; p < 2; ++p) h[c][p] = e[u][c][p] = __ffma2_rn(e[u][c][p], h[c][p], w[u][c][p]);
         };
-        if (!ALONE) recur();
+        if (!WHOLE) recur();
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int p = 0; p < 2; ++p) out[c][p] = !ALONE ? h[c][p] : __ffma2_rn(P[c][p], h[c][p], out[c][p]);
+            for (int p = 0; p < 2; ++p) out[c][p] = !WHOLE ? h[c][p] : __ffma2_rn(P[c][p], h[c][p], out[c][p]);
         // to the warp after
         if (i + 1 < turns) {
             const int to = warp + 1 == NW ? 0 : warp + 1;
@@ -288,7 +288,7 @@ scan_prompt_kernel(ScanServeArgs a) {
             if (dv && !(real::all_finite<4>(out[0]) && real::all_finite<4>(out[1])))
                 flag_if(a.status, kStatusNonFinite);
         }
-        if (ALONE) recur();
+        if (WHOLE) recur();
         // y: the lane's part of the sums over the states, then their reduction
         float yp[2 * U];  // [step][channel]
 #pragma unroll
@@ -533,28 +533,29 @@ __global__ void __launch_bounds__(256, 3) scan_step_batch_kernel(ScanServeArgs a
     if (dv && !(finite.x + finite.y == 0.f)) flag_if(a.status, kStatusNonFinite);
 }
 
-template <typename E, int N, bool ZOH, int FORM>
+template <typename E, int N, bool ZOH, bool MANY>
 cudaError_t prompt_launch(const ScanServeArgs& a, unsigned ctas, cudaStream_t st) {
-    scan_prompt_kernel<E, N, ZOH, FORM><<<ctas, PromptCfg<N, FORM>::NW * 32, 0, st>>>(a);
+    scan_prompt_kernel<E, N, ZOH, MANY><<<ctas, PromptCfg<N, MANY>::NW * 32, 0, st>>>(a);
     return cudaGetLastError();
 }
 
-// Measured on a B200 (N = 16, bf16, gated), in cycles a step of 16 channels: a CTA alone on its SM takes 130
-// (kMany), 42 (kFew) and 36 (kAlone); an SM full of CTAs 36 (kMany) and 53 (kFew).  kFew wins while its
-// throughput, 53 rows ndt / 148, stays below the time that the longest sequence takes in kMany,
-// 130 max_len: rows * ndt < 363 max_len.  kAlone wins while every CTA has an SM to itself.
+// The forms cross where the few form's throughput meets the time that the longest sequence takes in the many
+// form, that is at a fixed number of CTAs' worth of full-length work, rows * ndt / max_len.  Measured on a
+// B200 (bf16, gated; us many / few): N = 16 at 351 201 / 166, at 411 56 / 84, at 678 48 / 76; N = 8 at 245
+// 158 / 108, at 339 34 / 43; N = 4 at 192 41 / 34, at 429 16 / 34.
+template <int N> constexpr int64_t kManyFrom = N == 16 ? 363 : (N == 8 ? 300 : 250);
+
 template <typename E, int N, bool ZOH>
 cudaError_t prompt_impl(ScanServeArgs a, cudaStream_t st) {
-    a.ndt = (a.D + PromptCfg<N, kMany>::CW - 1) / PromptCfg<N, kMany>::CW;
+    a.ndt = (a.D + PromptCfg<N, true>::CW - 1) / PromptCfg<N, true>::CW;
     const int64_t ctas = (int64_t)a.S * a.ndt;
     // Worth it when there are more CTAs than run at once, few enough sequences to be ranked by every CTA, and
     // a longest one (36 cycles a step) that outweighs the ranking, 2 us a CTA.
     a.sorted = a.S > 1 && a.S <= 64 && ctas > 592 && a.max_len >= 512 &&
                (int64_t)a.max_len * a.S > 2 * (int64_t)a.rows;
-    if (ctas <= 148) return prompt_launch<E, N, ZOH, kAlone>(a, (unsigned)ctas, st);
-    if ((int64_t)a.rows * a.ndt < (int64_t)363 * a.max_len)
-        return prompt_launch<E, N, ZOH, kFew>(a, (unsigned)ctas, st);
-    return prompt_launch<E, N, ZOH, kMany>(a, (unsigned)ctas, st);
+    if ((int64_t)a.rows * a.ndt >= kManyFrom<N> * a.max_len)
+        return prompt_launch<E, N, ZOH, true>(a, (unsigned)ctas, st);
+    return prompt_launch<E, N, ZOH, false>(a, (unsigned)ctas, st);
 }
 
 template <typename E, int N>

@@ -527,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_prompt_kernel(ConvServeArgs 
         check_batch(a.offsets, a.slot, a.S, a.rows, a.slots, a.rows, a.status);
     int s = find_seq(a.offsets, a.S, a.G, item0);
     for (int k = 0; k < ty && s + 1 < a.S && item_base(a.offsets, s + 1, a.G) <= item; ++k) ++s;
+    const bool carried = a.carry && a.carry[s];  // on its way together with the offsets
     const Span sp = item_span(a.offsets, a.slot, s, a.G, item, a.rows, a.slots);
     __syncthreads();
     if (sp.ok && ty < a.ry && named_before(a.slot, sp.s, sp.slot, tx, a.cx)) repeated[ty] = 1;
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_prompt_kernel(ConvServeArgs 
     load_taps<W, V>(w, bias, a.w, a.bias, c);
     E* entry = sp.slot >= 0 ? static_cast<E*>(a.pool) + (size_t)sp.slot * (W - 1) * a.D + c : nullptr;
     if (sp.local == 0) {
-        const bool carry = entry && a.carry && a.carry[sp.s];
+        const bool carry = entry && carried;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {  // entry j is input j - (W-1): slot U - (W-1) + j
             float2 (&o)[P] = x[U - (W - 1) + j];

@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(ConvArgs a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (t + u >= t1) break;
-            R::unpack(ring[(stage * U + u) * kThreads], (ew >> (8 * u)) & 255u, x[u]);
+            R::unpack(ring[(stage * U + u) * kThreads], __byte_perm(ew, 0u, 0x4440 | u), x[u]);
             float2 v[P];
             preact<W, P>(v, w, bias, x, u);
             if (SILU) silu<P>(v);
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
         // one row: INNER when it is summed, writes a row of dx, and nothing touches the ends
         auto row = [&](int t, int u, int stage, auto inner) {
             constexpr bool INNER = decltype(inner)::value;
-            R::unpack(xring[(stage * U + u) * kThreads], (ew >> (8 * u)) & 255u, x[u]);
+            R::unpack(xring[(stage * U + u) * kThreads], __byte_perm(ew, 0u, 0x4440 | u), x[u]);
             Vec<E, 4>::unpack(gring[(stage * U + u) * kThreads], g[u]);  // dy, now to become dL/dv
             if (SILU) {
                 float2 v[2];

@@ -181,11 +181,11 @@ template <typename E> struct Rows<E, 4, true> {
     using Raw = unsigned;
     const int8_t* q;
     const uint8_t* e;
-    unsigned D;
+    unsigned ldb;  // D
     __device__ __forceinline__ Rows(const ConvArgs& a, int b, int c)
         : q(a.q + (size_t)b * a.L * a.D + c),
-          e(a.qe + ((size_t)b * ((a.D + 31) / 32) + c / 32) * a.Lq), D((unsigned)a.D) {}
-    __device__ __forceinline__ const void* at(int t) const { return row_at(q, t, D); }
+          e(a.qe + ((size_t)b * ((a.D + 31) / 32) + c / 32) * a.Lq), ldb((unsigned)a.D) {}
+    __device__ __forceinline__ const void* at(int t) const { return row_at(q, t, ldb); }
     __device__ __forceinline__ unsigned word(int t) const { return *reinterpret_cast<const unsigned*>(e + t); }
     static __device__ __forceinline__ void unpack(const Raw& r, unsigned e, float2 (&o)[2]) {
         restore4(o[0], o[1], r, e);
@@ -198,11 +198,11 @@ template <typename E> struct Rows<E, 8, true> {
     using Raw = uint2;
     const int8_t* q;
     const uint8_t* e;
-    unsigned D;
+    unsigned ldb;  // D
     __device__ __forceinline__ Rows(const ConvArgs& a, int b, int c)
         : q(a.q + (size_t)b * a.L * a.D + c),
-          e(a.qe + ((size_t)b * ((a.D + 31) / 32) + c / 32) * a.Lq), D((unsigned)a.D) {}
-    __device__ __forceinline__ const void* at(int t) const { return row_at(q, t, D); }
+          e(a.qe + ((size_t)b * ((a.D + 31) / 32) + c / 32) * a.Lq), ldb((unsigned)a.D) {}
+    __device__ __forceinline__ const void* at(int t) const { return row_at(q, t, ldb); }
     __device__ __forceinline__ unsigned word(int t) const { return *reinterpret_cast<const unsigned*>(e + t); }
     static __device__ __forceinline__ void unpack(const Raw& r, unsigned e, float2 (&o)[4]) {
         restore4(o[0], o[1], r.x, e);
@@ -370,13 +370,25 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
         const R rows(a, b, c);
         const E* dy = static_cast<const E*>(a.dy) + (size_t)b * a.L * a.lddy + c;
         const unsigned lddyb = (unsigned)(a.lddy * sizeof(E)), lddxb = (unsigned)(a.lddx * sizeof(E));
+        // Rows are issued in order, so their addresses are running sums (one addition a row instead of a
+        // wide product: 152 -> 145 us at 4 x 8192 x 4096, 168 -> 161 from 8 bits).
+        uintptr_t gp = (uintptr_t)row_at(dy, t0, lddyb), xp = (uintptr_t)rows.at(t0);
         auto issue = [&](int t, int stage) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (t + u < tend) {
-                    cp_async<sizeof(GRaw)>(gring + (stage * U + u) * kThreads, row_at(dy, t + u, lddyb));
-                    cp_async<sizeof(Raw)>(xring + (stage * U + u) * kThreads, rows.at(t + u));
+            auto one = [&](int u, bool there) {
+                if (there) {
+                    cp_async<sizeof(GRaw)>(gring + (stage * U + u) * kThreads, (const void*)gp);
+                    cp_async<sizeof(Raw)>(xring + (stage * U + u) * kThreads, (const void*)xp);
                 }
+                gp += lddyb;
+                xp += rows.ldb;
+            };
+            if (t + U <= tend) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) one(u, true);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) one(u, t + u < tend);
+            }
             cp_async_commit();
         };
 #pragma unroll
@@ -398,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
                 rows.load(t0 - j, x[U - j]);
             g[U - j][0] = g[U - j][1] = make_float2(0.f, 0.f);
         }
+        uintptr_t dp = (uintptr_t)dx + (unsigned long long)t0 * lddxb - (unsigned long long)(W - 1) * lddxb;
         // one row: INNER when it is summed, writes a row of dx, and nothing touches the ends
         auto row = [&](int t, int u, int stage, auto inner) {
             constexpr bool INNER = decltype(inner)::value;
@@ -442,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
                 d[1] = __fadd2_rn(d[1], e[1]);
             }
             if (INNER || r >= 0)
-                st_vec<E, 4>(row_at(dx, r, lddxb), d);
+                st_vec<E, 4>(reinterpret_cast<E*>(dp + (unsigned long long)u * lddxb), d);
             else if (ds0)
                 st_vec<E, 4>(ds0 + (size_t)(r + W - 1) * a.D, d);
         };
@@ -460,6 +473,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
                 for (int u = 0; u < U; ++u) row(t + u, u, stage, std::false_type{});
             }
             ew = en;
+            dp += (unsigned long long)U * lddxb;
             stage = stage == DEPTH - 1 ? 0 : stage + 1;
         }
     }

@@ -53,8 +53,9 @@ Tile tile_of(int D, int V) {
     return t;
 }
 
-// The taps of V channels, tap-major: w[j][pair].
-template <int W, int V>
+// The taps of V channels, tap-major: w[j][pair].  With SiLU they and the bias are scaled by log2 e, so that
+// the pre-activation comes out as v log2 e, the argument of its exp2 (see silu and conv_bwd_kernel).
+template <int W, int V, bool SILU>
 __device__ __forceinline__ void load_taps(float2 (&w)[W][V / 2], float2 (&bias)[V / 2], const float* pw,
                                           const float* pb, int c) {
     float f[V * W];
@@ -68,6 +69,12 @@ __device__ __forceinline__ void load_taps(float2 (&w)[W][V / 2], float2 (&bias)[
 #pragma unroll
         for (int j = 0; j < W; ++j) w[j][p] = make_float2(f[2 * p * W + j], f[(2 * p + 1) * W + j]);
         bias[p] = pb ? __ldg(reinterpret_cast<const float2*>(pb + c) + p) : make_float2(0.f, 0.f);
+        if (SILU) {
+            const float2 k = make_float2(kLog2e, kLog2e);
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][p] = __fmul2_rn(w[j][p], k);
+            bias[p] = __fmul2_rn(bias[p], k);
+        }
     }
 }
 
@@ -83,10 +90,18 @@ __device__ __forceinline__ void preact(float2 (&v)[P], const float2 (&w)[W][P], 
     }
 }
 
+// ln 2 sigmoid(v) of a pair from u = v log2 e: 1 / (log2 e (1 + 2^-u)), one fused operation and the two
+// special functions.  2^-u overflows below v = -88, where the quotient is zero.
+__device__ __forceinline__ float2 sigmoid_ln2(float2 u) {
+    const float2 k = make_float2(kLog2e, kLog2e);
+    const float2 a = __ffma2_rn(make_float2(ex2_mufu(-u.x), ex2_mufu(-u.y)), k, k);
+    return make_float2(rcp_mufu(a.x), rcp_mufu(a.y));
+}
+// v sigmoid(v) = u (ln 2 sigmoid(v))
 template <int P>
-__device__ __forceinline__ void silu(float2 (&v)[P]) {
+__device__ __forceinline__ void silu(float2 (&u)[P]) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) v[p] = silu_pair(v[p]);
+    for (int p = 0; p < P; ++p) u[p] = __fmul2_rn(u[p], sigmoid_ln2(u[p]));
 }
 
 // ---------------------------------------------------------------- 8-bit checkpoint
@@ -265,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(ConvArgs a) {
     unsigned ew = SRC8 && t0 < t1 ? rows.word(t0) : 0u;
 
     float2 w[W][P], bias[P], x[U][P];
-    load_taps<W, V>(w, bias, a.w, a.bias, cc);
+    load_taps<W, V, SILU>(w, bias, a.w, a.bias, cc);
     const E* s0 = a.s0 ? static_cast<const E*>(a.s0) + (size_t)b * (W - 1) * a.D + cc : nullptr;
 #pragma unroll
     for (int j = 1; j < W; ++j) {
@@ -396,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
         unsigned ew = SRC8 && t0 < tend ? rows.word(t0) : 0u;
 
         float2 w[W][2], bias[2], x[U][2], g[U][2];
-        load_taps<W, 4>(w, bias, a.w, a.bias, c);
+        load_taps<W, 4, SILU>(w, bias, a.w, a.bias, c);
         const size_t so = (size_t)b * (W - 1) * a.D + c;
         const E* s0 = a.s0 ? static_cast<const E*>(a.s0) + so : nullptr;
         const E* dsL = a.dsL ? static_cast<const E*>(a.dsL) + so : nullptr;
@@ -421,11 +436,11 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
                 preact<W, 2>(v, w, bias, x, u);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    // d (v s) / dv = s (1 + v (1 - s))
-                    const float2 one = make_float2(1.f, 1.f);
-                    const float2 s = sigmoid_pair(v[p]);
-                    const float2 r = __ffma2_rn(s, make_float2(-1.f, -1.f), one);
-                    g[u][p] = __fmul2_rn(g[u][p], __fmul2_rn(s, __ffma2_rn(v[p], r, one)));
+                    // ln 2 d (v s) / dv = ln 2 s (1 + v (1 - s)), with v (1 - s) = v log2 e (ln 2 - ln 2 s).
+                    // The factor ln 2 cancels against the taps' log2 e in dx; the sums get it back at the end.
+                    const float2 s = sigmoid_ln2(v[p]);
+                    const float2 r = __ffma2_rn(s, make_float2(-1.f, -1.f), make_float2(kLn2, kLn2));
+                    g[u][p] = __fmul2_rn(g[u][p], __fmul2_rn(s, __ffma2_rn(v[p], r, make_float2(1.f, 1.f))));
                 }
             }
             if (!INNER && t >= tend) g[u][0] = g[u][1] = make_float2(0.f, 0.f);  // the ring holds other rows
@@ -494,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
         if (ch >= a.D) continue;
         float v = 0.f;
         for (int r = 0; r < a.ry; ++r) v += red[(j * a.ry + r) * wid + k];
-        a.part[((size_t)blockIdx.x * (W + 1) + j) * a.D + ch] = v;
+        a.part[((size_t)blockIdx.x * (W + 1) + j) * a.D + ch] = SILU ? v * kLog2e : v;
     }
 }
 
@@ -565,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_prompt_kernel(ConvServeArgs 
 #pragma unroll
     for (int k = 0; k < DEPTH - 1; ++k) issue(t0 + k * U, k);
     float2 w[W][P], bias[P], x[U][P];
-    load_taps<W, V>(w, bias, a.w, a.bias, c);
+    load_taps<W, V, SILU>(w, bias, a.w, a.bias, c);
     E* entry = sp.slot >= 0 ? static_cast<E*>(a.pool) + (size_t)sp.slot * (W - 1) * a.D + c : nullptr;
     if (sp.local == 0) {
         const bool carry = entry && carried;
@@ -638,7 +653,7 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvServeArgs a) {
                              : Vec<E, 4>::zero();
     }
     float2 w[W][2], bias[2];
-    load_taps<W, 4>(w, bias, a.w, a.bias, cv ? c : 0);
+    load_taps<W, 4, SILU>(w, bias, a.w, a.bias, cv ? c : 0);
     if (a.slot) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {

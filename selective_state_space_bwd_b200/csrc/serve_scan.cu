@@ -36,6 +36,14 @@ __device__ __forceinline__ float4 quad_f4(const typename Vec<E, 4>::Raw& r) {
     return make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
 }
 
+// A log2(e) of a pair of states, finite even where exp(A_log) is not: there a step of any length still leaves
+// nothing of the state, but a step of length zero (past the end of a sequence, inside its last turn) all of it.
+// A NaN stays.
+__device__ __forceinline__ float2 rate_pair(float l0, float l1) {
+    const float a = expf(l0) * kLog2e, b = expf(l1) * kLog2e, top = 3.402823466e38f;
+    return make_float2(a > top ? -top : -a, b > top ? -top : -b);
+}
+
 // w B x for a pair of states: delta and delta x (each twice), e = exp(delta A), A2 = A log2(e), Ar = 1 / A
 template <bool ZOH>
 __device__ __forceinline__ float2 input_term(float2 dlt, float2 dx, float2 e, float2 A2, float2 Ar, float2 bq) {
@@ -178,8 +186,8 @@ scan_prompt_kernel(ScanServeArgs a) {
     float2 A2[2][2], Ar[2][2];  // [channel][pair of states]
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        A2[c][0] = make_float2(-expf(l[c].x) * kLog2e, -expf(l[c].y) * kLog2e);
-        A2[c][1] = make_float2(-expf(l[c].z) * kLog2e, -expf(l[c].w) * kLog2e);
+        A2[c][0] = rate_pair(l[c].x, l[c].y);
+        A2[c][1] = rate_pair(l[c].z, l[c].w);
         if (ZOH) {
             Ar[c][0] = make_float2(-expf(-l[c].x), -expf(-l[c].y));
             Ar[c][1] = make_float2(-expf(-l[c].z), -expf(-l[c].w));
@@ -323,8 +331,8 @@ struct StepRow {  // what one row adds to the state
 template <bool ZOH>
 __device__ __forceinline__ StepRow step_consts(float4 l, float dsk) {
     StepRow c;
-    c.A2[0] = make_float2(-expf(l.x) * kLog2e, -expf(l.y) * kLog2e);
-    c.A2[1] = make_float2(-expf(l.z) * kLog2e, -expf(l.w) * kLog2e);
+    c.A2[0] = rate_pair(l.x, l.y);
+    c.A2[1] = rate_pair(l.z, l.w);
     if (ZOH) {
         c.Ar[0] = make_float2(-expf(-l.x), -expf(-l.y));
         c.Ar[1] = make_float2(-expf(-l.z), -expf(-l.w));

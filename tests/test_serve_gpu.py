@@ -350,6 +350,35 @@ def test_nonfinite_state_is_reported(S):
     assert S.ssm_scan_status(ws) == 0
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("zoh", [False, True])
+@pytest.mark.parametrize("N", [4, 8, 16])
+def test_decay_rates_past_the_largest_number(S, oracle_mod, N, zoh, io):
+    """exp(A_log) past fp32's range: such a state keeps nothing of the step before, in turns that the
+    sequence's end leaves partly empty as well, and in single tokens."""
+    lens, D = [1, 13, 30, 3], 40
+    t = batch(lens, D, N, 4, io, N, [3, 0, 1, 2], 4)
+    t["A_log"][3, 2], t["A_log"][8, 0], t["A_log"][39] = 100.0, 89.0, 200.0
+    on = torch.ones(4, dtype=torch.bool, device="cuda")
+    args = [t[k] for k in ("x", "delta_raw", "A_log", "Bm", "Cm", "Dskip")]
+    n = [f64(a) for a in args]
+    for max_len in (0, 30):
+        pool, ws = t["spool"].clone(), torch.empty(256, dtype=torch.uint8, device="cuda")
+        y = torch.full((t["x"].shape[0], D), 7, dtype=DT[io], device="cuda")
+        S.ssm_scan_prompt(*args, t["offsets"], t["slots"], pool, carry=on, zoh=zoh, max_len=max_len, y=y, ws=ws)
+        assert S.ssm_scan_status(ws) == S.SSM_OK
+        ry, rp = oracle_mod.scan_serve(*n, host(t["offsets"]), [3, 0, 1, 2], f64(t["spool"]), host(on), None, zoh,
+                                       y=7.0)
+        check_prompt(y, pool, ry, rp, t, io, 1e-5, 1e-5)
+    pool = t["spool"].clone()
+    rows = [a[:4] if a.shape[0] == t["x"].shape[0] else a for a in args]
+    y = S.ssm_scan_step(*rows, t["slots"], pool, zoh=zoh)
+    ry, rp = oracle_mod.scan_serve(*[f64(a) for a in rows], np.arange(5, dtype=np.int32), [3, 0, 1, 2],
+                                   f64(t["spool"]), np.ones(4, bool), None, zoh)
+    close(y, ry, io, "y", 1e-5)
+    close(pool, rp, "f32", "pool", 1e-5)
+
+
 def test_prompt_then_tokens_equal_the_dense_forward(S):
     """A prompt split over three calls and then single tokens, through convolution and scan, give what
     the dense training forward gives for the whole sequence."""

@@ -482,9 +482,11 @@ int ssm_conv_bwd(const ssm_conv_shape* shape, const void* x, const int8_t* q, co
  * slot are out of range, one longer than max_len, and each that names an entry which an earlier one of
  * the same call names too is left out (its rows of y and its entry stay as they are), and
  * SSM_ERR_INVALID_ARG is recorded in the status word.  SSM_ERR_NONFINITE is recorded as for the
- * other scans.  (Offsets that run backwards can also make the rows of two sequences overlap; then it is
- * not determined which of the two wrote them.)  ws may be NULL (ws_bytes 0) where a call needs only the status word (256 bytes): then
- * nothing is recorded, and the call is one kernel with no memset before it.
+ * other scans.  Behind the first offset that runs backwards or leaves 0..rows it is not determined which rows
+ * and entries of the later sequences a call writes (none but theirs); the sequences before it are whole, but for
+ * rows that a later one claims too.
+ * ws (256 bytes) holds the status word alone and may be NULL (ws_bytes 0): then nothing is recorded, and
+ * the call is one kernel with no memset before it.
  *
  * Which kernel runs depends on the batch's sizes: repeats are bitwise equal, and a sequence's results in
  * different batches, or cut into several calls, agree to rounding (the convolution's are bitwise equal).

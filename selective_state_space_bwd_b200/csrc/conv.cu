@@ -438,6 +438,8 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
                 for (int p = 0; p < 2; ++p) {
                     // ln 2 d (v s) / dv = ln 2 s (1 + v (1 - s)), with v (1 - s) = v log2 e (ln 2 - ln 2 s).
                     // The factor ln 2 cancels against the taps' log2 e in dx; the sums get it back at the end.
+                    // (Of v from 18 on the sum under sigmoid_ln2's quotient is log2 e to the bit, and the quotient
+                    // kLn2 to the bit, so that r is zero however large v is.)
                     const float2 s = sigmoid_ln2(v[p]);
                     const float2 r = __ffma2_rn(s, make_float2(-1.f, -1.f), make_float2(kLn2, kLn2));
                     g[u][p] = __fmul2_rn(g[u][p], __fmul2_rn(s, __ffma2_rn(v[p], r, make_float2(1.f, 1.f))));

@@ -246,6 +246,37 @@ def test_conv_infinities_stay_where_they_are(S):
     assert torch.equal(g["dbias"].isnan(), only) and torch.equal(g["dw"].isnan().any(1), only)
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [1e2, 1e4, 1e7, 1e12])
+def test_conv_of_large_preactivations(S, size, io):
+    """SiLU far from zero is the identity, or nothing: so are its values and gradients, at any size.  From v =
+    100 on 1 - sigmoid is below 1e-40.  A value is W + 1 products with rounded taps, and SiLU's exp2 and
+    quotient (2 u), two constants and two products; a gradient W products, the same and dy's own."""
+    B, L, D, W = 2, 37, 72, 4
+    g = torch.Generator().manual_seed(5)
+    x = (size * (1 + torch.rand(B, L, D, generator=g))).to(DT[io]).cuda()
+    dy = torch.randn(B, L, D, generator=g).to(DT[io]).cuda()
+    w = (0.5 + torch.rand(D, W, generator=g)).cuda() * 2
+    s0 = x[:, :W - 1].contiguous()
+    xs = torch.cat([s0, x], 1).double()
+    y = S.ssm_conv_fwd(x, w, s0=s0)[0]
+    v = sum(w[:, j].double() * xs[:, j:j + L] for j in range(W))
+    h = 2.0 ** -8 if io == "bf16" else 0.0
+    assert bool(((y.double() - v).abs() <= (2 * (W + 1 + 8) * U + h) * v).all())
+    r = S.ssm_conv_bwd(x, w, None, dy, s0=s0)
+    gp = torch.cat([dy.double(), torch.zeros(B, W - 1, D, dtype=torch.float64, device="cuda")], 1)
+    dx = sum(w[:, W - 1 - k].double() * gp[:, k:k + L] for k in range(W))
+    mag = sum(w[:, W - 1 - k].double() * gp[:, k:k + L].abs() for k in range(W))
+    assert bool(((r["dx"].double() - dx).abs() <= 2 * (W + 8) * U * mag + h * dx.abs()).all())
+    for j in range(W):
+        d = (dy.double() * xs[:, j:j + L])
+        assert bool(((r["dw"][:, j].double() - d.sum((0, 1))).abs() <= 2 * (B * L + 8) * U * d.abs().sum((0, 1))).all())
+    q8 = S.ssm_conv_fwd(x, w, s0=s0, want_q8=True)[2]
+    assert torch.equal(S.ssm_conv_bwd(None, w, None, dy, s0=s0, q8=q8)["dx"], r["dx"])  # dx does not depend on x here
+    down = S.ssm_conv_bwd(-x, w, None, dy, s0=-s0)
+    assert not S.ssm_conv_fwd(-x, w, s0=-s0)[0].any() and not down["dx"].any() and not down["dw"].any()
+
+
 def test_conv_past_two_to_the_31_elements(S):
     B, L, D, W = 1, 2 ** 31 // 4096 + 100, 4096, 4
     x = torch.empty(B, L, D, dtype=torch.bfloat16, device="cuda")

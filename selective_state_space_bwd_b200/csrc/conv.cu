@@ -26,19 +26,9 @@ constexpr int kThreads = 256;
 constexpr int kResident = 296;   // CTAs of a wave: two per SM (registers, and the ring)
 constexpr int U = 4;             // rows a group; row t of a piece that starts at t0 lies in slot (t - t0) % 4
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async(void* smem_dst, const void* gmem_src) {
-    const unsigned s = (unsigned)__cvta_generic_to_shared(smem_dst);
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(gmem_src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(s), "l"(gmem_src), "n"(BYTES) : "memory");
-}
+using real::cp_async;
 using real::cp_async_commit;
-template <int PENDING>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;\n" ::"n"(PENDING) : "memory");
-}
+using real::cp_async_wait;
 
 struct Tile {
     int cx, ry, nct;

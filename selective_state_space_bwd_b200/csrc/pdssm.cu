@@ -225,7 +225,7 @@ __device__ __forceinline__ void warp_entries(void* dst, const void* src, size_t 
             const unsigned sa = (unsigned)__cvta_generic_to_shared(d + ent * ds + k);
             const int n = e < total ? 4 : 0;
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(sa),
-                         "l"(n ? s + e : s), "r"(n));
+                         "l"(n ? s + e : s), "r"(n) : "memory");
         }
     }
 }
@@ -650,7 +650,7 @@ __device__ __forceinline__ void tile_sel(int* dst, const int32_t* src, size_t fi
         const unsigned sa = (unsigned)__cvta_generic_to_shared(dst + q);
         const int n = e < total ? 4 : 0;
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(sa),
-                     "l"(n ? src + e : src), "r"(n));
+                     "l"(n ? src + e : src), "r"(n) : "memory");
     }
 }
 

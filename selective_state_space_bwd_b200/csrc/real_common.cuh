@@ -142,16 +142,29 @@ __device__ __forceinline__ void reduce_scatter(float (&v)[V], int ng) {
 
 
 // ---------------------------------------------------------------- asynchronous copies (LDGSTS)
+// Every copy, commit and wait tells the compiler that it touches memory: a thread that reads its own copies
+// after its own wait, without a barrier in between (the rings of the convolution and of the single
+// tokens), has nothing else that keeps the reads behind the wait and the next copies behind the reads.
+
 // 16 bytes global -> shared; with valid == false nothing is read and the destination is zeroed.
 __device__ __forceinline__ void cp_async16(void* smem_dst, const void* gmem_src, bool valid) {
     const unsigned s = (unsigned)__cvta_generic_to_shared(smem_dst);
     const int n = valid ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(gmem_src), "r"(n));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(gmem_src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::); }
+// BYTES (16, 8 or 4) global -> shared.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* smem_dst, const void* gmem_src) {
+    const unsigned s = (unsigned)__cvta_generic_to_shared(smem_dst);
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(gmem_src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(s), "l"(gmem_src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int PENDING>
 __device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;\n" ::"n"(PENDING));
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(PENDING) : "memory");
 }
 
 // Asynchronously copy rows [t0, t0 + rows) x columns [c0, c0 + COLS) of a row-major [*, ncol]
@@ -188,11 +201,11 @@ __device__ __forceinline__ void cp_async_pieces(E* __restrict__ dst, const E* __
         const unsigned s = (unsigned)__cvta_generic_to_shared(dst + i * VEC);
         const E* g = bytes > 0 ? src + e : src;
         if (G == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(g), "r"(bytes));
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(g), "r"(bytes) : "memory");
         else if (G == 8)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(s), "l"(g), "r"(bytes));
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(s), "l"(g), "r"(bytes) : "memory");
         else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(s), "l"(g), "r"(bytes));
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(s), "l"(g), "r"(bytes) : "memory");
     }
 }
 template <typename E>

@@ -43,9 +43,8 @@ Tile tile_of(int D, int V) {
     return t;
 }
 
-// The taps of V channels, tap-major: w[j][pair].  With SiLU they and the bias are scaled by log2 e, so that
-// the pre-activation comes out as v log2 e, the argument of its exp2 (see silu and conv_bwd_kernel).
-template <int W, int V, bool SILU>
+// The taps of V channels, tap-major: w[j][pair].
+template <int W, int V>
 __device__ __forceinline__ void load_taps(float2 (&w)[W][V / 2], float2 (&bias)[V / 2], const float* pw,
                                           const float* pb, int c) {
     float f[V * W];
@@ -59,16 +58,12 @@ __device__ __forceinline__ void load_taps(float2 (&w)[W][V / 2], float2 (&bias)[
 #pragma unroll
         for (int j = 0; j < W; ++j) w[j][p] = make_float2(f[2 * p * W + j], f[(2 * p + 1) * W + j]);
         bias[p] = pb ? __ldg(reinterpret_cast<const float2*>(pb + c) + p) : make_float2(0.f, 0.f);
-        if (SILU) {
-            const float2 k = make_float2(kLog2e, kLog2e);
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[j][p] = __fmul2_rn(w[j][p], k);
-            bias[p] = __fmul2_rn(bias[p], k);
-        }
     }
 }
 
-// The pre-activation of the row in slot u from the rows in the slots before it.
+// The pre-activation of the row in slot u from the rows in the slots before it.  (Taps scaled by log2 e, which
+// would spare SiLU the product in front of its exp2, took 376 us against 381 for the training calls at 4 x 8192 x
+// 4096 from 8 bits.  They were taken out: a finite pre-activation past 2.36e38 became infinite, its gradient NaN.)
 template <int W, int P>
 __device__ __forceinline__ void preact(float2 (&v)[P], const float2 (&w)[W][P], const float2 (&bias)[P],
                                        const float2 (&x)[U][P], int u) {
@@ -80,18 +75,10 @@ __device__ __forceinline__ void preact(float2 (&v)[P], const float2 (&w)[W][P], 
     }
 }
 
-// ln 2 sigmoid(v) of a pair from u = v log2 e: 1 / (log2 e (1 + 2^-u)), one fused operation and the two
-// special functions.  2^-u overflows below v = -88, where the quotient is zero.
-__device__ __forceinline__ float2 sigmoid_ln2(float2 u) {
-    const float2 k = make_float2(kLog2e, kLog2e);
-    const float2 a = __ffma2_rn(make_float2(ex2_mufu(-u.x), ex2_mufu(-u.y)), k, k);
-    return make_float2(rcp_mufu(a.x), rcp_mufu(a.y));
-}
-// v sigmoid(v) = u (ln 2 sigmoid(v))
 template <int P>
-__device__ __forceinline__ void silu(float2 (&u)[P]) {
+__device__ __forceinline__ void silu(float2 (&v)[P]) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) u[p] = __fmul2_rn(u[p], sigmoid_ln2(u[p]));
+    for (int p = 0; p < P; ++p) v[p] = silu_pair(v[p]);
 }
 
 // ---------------------------------------------------------------- 8-bit checkpoint
@@ -270,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(ConvArgs a) {
     unsigned ew = SRC8 && t0 < t1 ? rows.word(t0) : 0u;
 
     float2 w[W][P], bias[P], x[U][P];
-    load_taps<W, V, SILU>(w, bias, a.w, a.bias, cc);
+    load_taps<W, V>(w, bias, a.w, a.bias, cc);
     const E* s0 = a.s0 ? static_cast<const E*>(a.s0) + (size_t)b * (W - 1) * a.D + cc : nullptr;
 #pragma unroll
     for (int j = 1; j < W; ++j) {
@@ -401,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
         unsigned ew = SRC8 && t0 < tend ? rows.word(t0) : 0u;
 
         float2 w[W][2], bias[2], x[U][2], g[U][2];
-        load_taps<W, 4, SILU>(w, bias, a.w, a.bias, c);
+        load_taps<W, 4>(w, bias, a.w, a.bias, c);
         const size_t so = (size_t)b * (W - 1) * a.D + c;
         const E* s0 = a.s0 ? static_cast<const E*>(a.s0) + so : nullptr;
         const E* dsL = a.dsL ? static_cast<const E*>(a.dsL) + so : nullptr;
@@ -426,13 +413,12 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
                 preact<W, 2>(v, w, bias, x, u);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    // ln 2 d (v s) / dv = ln 2 s (1 + v (1 - s)), with v (1 - s) = v log2 e (ln 2 - ln 2 s).
-                    // The factor ln 2 cancels against the taps' log2 e in dx; the sums get it back at the end.
-                    // (Of v from 18 on the sum under sigmoid_ln2's quotient is log2 e to the bit, and the quotient
-                    // kLn2 to the bit, so that r is zero however large v is.)
-                    const float2 s = sigmoid_ln2(v[p]);
-                    const float2 r = __ffma2_rn(s, make_float2(-1.f, -1.f), make_float2(kLn2, kLn2));
-                    g[u][p] = __fmul2_rn(g[u][p], __fmul2_rn(s, __ffma2_rn(v[p], r, make_float2(1.f, 1.f))));
+                    // d (v s) / dv = s (1 + v (1 - s)).  Of v from 18 on s is one to the bit, so that the difference
+                    // is zero however large v is.
+                    const float2 one = make_float2(1.f, 1.f);
+                    const float2 s = sigmoid_pair(v[p]);
+                    const float2 r = __ffma2_rn(s, make_float2(-1.f, -1.f), one);
+                    g[u][p] = __fmul2_rn(g[u][p], __fmul2_rn(s, __ffma2_rn(v[p], r, one)));
                 }
             }
             if (!INNER && t >= tend) g[u][0] = g[u][1] = make_float2(0.f, 0.f);  // the ring holds other rows
@@ -501,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
         if (ch >= a.D) continue;
         float v = 0.f;
         for (int r = 0; r < a.ry; ++r) v += red[(j * a.ry + r) * wid + k];
-        a.part[((size_t)blockIdx.x * (W + 1) + j) * a.D + ch] = SILU ? v * kLog2e : v;
+        a.part[((size_t)blockIdx.x * (W + 1) + j) * a.D + ch] = v;
     }
 }
 
@@ -572,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_prompt_kernel(ConvServeArgs 
 #pragma unroll
     for (int k = 0; k < DEPTH - 1; ++k) issue(t0 + k * U, k);
     float2 w[W][P], bias[P], x[U][P];
-    load_taps<W, V, SILU>(w, bias, a.w, a.bias, c);
+    load_taps<W, V>(w, bias, a.w, a.bias, c);
     E* entry = sp.slot >= 0 ? static_cast<E*>(a.pool) + (size_t)sp.slot * (W - 1) * a.D + c : nullptr;
     if (sp.local == 0) {
         const bool carry = entry && carried;
@@ -645,7 +631,7 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvServeArgs a) {
                              : Vec<E, 4>::zero();
     }
     float2 w[W][2], bias[2];
-    load_taps<W, 4, SILU>(w, bias, a.w, a.bias, cv ? c : 0);
+    load_taps<W, 4>(w, bias, a.w, a.bias, cv ? c : 0);
     if (a.slot) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {

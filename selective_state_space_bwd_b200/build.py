@@ -1,9 +1,11 @@
 """Build libssm_scan.so (all CUDA sources under csrc/) for sm_100a with nvcc, and the compiled binding
-_ssm_torch.so (csrc/binding.cpp) with the host compiler, in-tree."""
+_ssm_torch.so (csrc/binding.cpp) with the host compiler, in-tree.  The library needs nvcc alone; the binding, which
+only Python programs with torch use, is left out where torch is not installed, or with ``--library``."""
 
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -33,8 +35,12 @@ def _newer(out, ins) -> bool:
     return os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in ins)
 
 
-def up_to_date() -> bool:
-    return _newer(LIB, deps()) and _newer(BINDING, binding_deps())
+def _has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
+def up_to_date(binding: bool = True) -> bool:
+    return _newer(LIB, deps()) and not (binding and _has_torch() and not _newer(BINDING, binding_deps()))
 
 
 def _binding_commands(obj):
@@ -54,10 +60,11 @@ def _binding_commands(obj):
              "-lc10", "-lc10_cuda", "-L" + HERE, "-l:libssm_scan.so", "-Wl,-rpath,$ORIGIN"])
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
+def build(force: bool = False, verbose: bool = False, binding: bool = True) -> str:
     """Compile every source whose object is stale to an object, in parallel (one nvcc process
-    each; no device code crosses files), then link the shared library and, against it, the binding."""
-    if not force and up_to_date():
+    each; no device code crosses files), then link the shared library and, against it, the binding.
+    An error of the binding's is raised once the library is in place."""
+    if not force and up_to_date(binding):
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
     obj_dir = os.path.join(HERE, "_build")
@@ -75,17 +82,24 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     procs = [subprocess.Popen([nvcc, *flags, "-c", src, "-o", obj])
              for src, obj in zip(sources(), objs) if stale(src, obj)]
-    link = None
-    if force or not _newer(BINDING, binding_deps()):
-        compile_, link = _binding_commands(os.path.join(obj_dir, "binding.o"))
-        procs.append(subprocess.Popen(compile_))
+    link = compiling = error = None
+    if binding and _has_torch() and (force or not _newer(BINDING, binding_deps())):
+        try:
+            compile_, link = _binding_commands(os.path.join(obj_dir, "binding.o"))
+            compiling = subprocess.Popen(compile_)
+        except Exception as e:  # a torch that does not import, no compiler: the library comes first
+            error = e
     failed = [p.args for p in procs if p.wait() != 0]
+    if compiling and compiling.wait() != 0:
+        error = subprocess.CalledProcessError(1, compiling.args)
     if failed:
         raise subprocess.CalledProcessError(1, failed[0])
     if force or not _newer(LIB, [*deps(), *objs]):
         subprocess.run([nvcc, *ARCH, "-shared", "-Xlinker", "-soname=libssm_scan.so", "-o", LIB + ".tmp", *objs],
                        check=True)
         os.replace(LIB + ".tmp", LIB)
+    if error:
+        raise error
     if link:
         subprocess.run(link, check=True)
         os.replace(BINDING + ".tmp", BINDING)
@@ -93,5 +107,5 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    build(force=True, verbose="-v" in sys.argv)
+    build(force=True, verbose="-v" in sys.argv, binding="--library" not in sys.argv)
     print(LIB)

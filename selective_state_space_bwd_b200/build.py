@@ -15,6 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libssm_scan.so")
 BINDING = os.path.join(HERE, "_ssm_torch.so")
+BINDING_KEY = os.path.join(HERE, "_build", "binding.key")  # binding_key() of the binding that is there
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -39,8 +40,27 @@ def _has_torch() -> bool:
     return importlib.util.find_spec("torch") is not None
 
 
+def binding_key() -> str:
+    """What a compiled binding belongs to: torch's version and C++ ABI, and the Python's ABI."""
+    import sysconfig
+
+    import torch
+    return (f"torch {torch.__version__}, C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, "
+            f"Python {sysconfig.get_config_var('SOABI')}")
+
+
+def _binding_up_to_date() -> bool:
+    if not _newer(BINDING, binding_deps()) or not os.path.exists(BINDING_KEY):
+        return False
+    try:
+        with open(BINDING_KEY) as f:
+            return f.read() == binding_key()
+    except Exception:  # a torch that does not import: the build says so, behind the library
+        return False
+
+
 def up_to_date(binding: bool = True) -> bool:
-    return _newer(LIB, deps()) and not (binding and _has_torch() and not _newer(BINDING, binding_deps()))
+    return _newer(LIB, deps()) and not (binding and _has_torch() and not _binding_up_to_date())
 
 
 def _binding_commands(obj):
@@ -55,7 +75,7 @@ def _binding_commands(obj):
     cxx = os.environ.get("CXX", "g++")
     return ([cxx, "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden",
              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-             "-DTORCH_EXTENSION_NAME=_ssm_torch", *[f"-isystem{p}" for p in inc], "-c", binding_deps()[0], "-o", obj],
+             "-DTORCH_EXTENSION_NAME=_ssm_torch", f'-DSSM_BUILT_AGAINST="{binding_key()}"', *[f"-isystem{p}" for p in inc], "-c", binding_deps()[0], "-o", obj],
             [cxx, "-shared", obj, "-o", BINDING + ".tmp", f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
              "-lc10", "-lc10_cuda", "-L" + HERE, "-l:libssm_scan.so", "-Wl,-rpath,$ORIGIN"])
 
@@ -83,7 +103,7 @@ def build(force: bool = False, verbose: bool = False, binding: bool = True) -> s
     procs = [subprocess.Popen([nvcc, *flags, "-c", src, "-o", obj])
              for src, obj in zip(sources(), objs) if stale(src, obj)]
     link = compiling = error = None
-    if binding and _has_torch() and (force or not _newer(BINDING, binding_deps())):
+    if binding and _has_torch() and (force or not _binding_up_to_date()):
         try:
             compile_, link = _binding_commands(os.path.join(obj_dir, "binding.o"))
             compiling = subprocess.Popen(compile_)
@@ -103,6 +123,8 @@ def build(force: bool = False, verbose: bool = False, binding: bool = True) -> s
     if link:
         subprocess.run(link, check=True)
         os.replace(BINDING + ".tmp", BINDING)
+        with open(BINDING_KEY, "w") as f:
+            f.write(binding_key())
     return LIB
 
 

@@ -299,6 +299,7 @@ Tensor scan_serve(const Tensor& x, const Tensor& delta_raw, const Tensor& A_log,
 }  // namespace
 
 PYBIND11_MODULE(_ssm_torch, m) {
+    m.attr("built_against") = SSM_BUILT_AGAINST;  // compared before the first call
     m.def("set_error_class", [](py::object c) { error_class() = std::move(c); });
     m.def("conv_fwd", &conv_fwd);
     m.def("conv_restore", &conv_restore);

@@ -572,7 +572,8 @@ _torch_binding = None
 
 
 def _native():
-    """The compiled binding of these calls, _ssm_torch.so (opened once).  Raises if it has not been built."""
+    """The compiled binding of these calls, _ssm_torch.so (opened once).  Raises if it has not been built, or not
+    against this torch."""
     global _torch_binding
     if _torch_binding is None:
         if not os.path.exists(os.path.join(_HERE, "_ssm_torch.so")):
@@ -580,6 +581,11 @@ def _native():
                                "`python -m selective_state_space_bwd_b200.build` (no CPU fallback)")
         lib()
         from . import _ssm_torch as b
+        from .build import binding_key
+        against = getattr(b, "built_against", "an unknown torch")
+        if against != binding_key():
+            raise RuntimeError(f"{_HERE}/_ssm_torch.so was built against {against}, this is {binding_key()}: "
+                               "build it again with `python -m selective_state_space_bwd_b200.build`")
         b.set_error_class(SsmError)
         _torch_binding = b
     return _torch_binding

@@ -110,3 +110,42 @@ def test_the_library_alone_on_demand(tree):
     assert tree.lib.exists() and not tree.runs("cxx") and not b.up_to_date()
     b.build(binding=False)
     assert len(tree.runs("nvcc")) == 3
+
+
+def test_another_torch_or_python_makes_the_binding_anew(tree, monkeypatch):
+    """The binding is compiled against one torch, C++ ABI and Python: under another it is not up to date."""
+    import sysconfig
+
+    import torch
+    b = tree.load()
+    b.build()
+    assert b.up_to_date() and len(tree.runs("cxx")) == 2
+    real = sysconfig.get_config_var
+    for n, change in enumerate((lambda m: m.setattr(torch, "__version__", "0.0.1"),
+                                lambda m: m.setattr(torch._C, "_GLIBCXX_USE_CXX11_ABI",
+                                                    not torch._C._GLIBCXX_USE_CXX11_ABI),
+                                lambda m: m.setattr(sysconfig, "get_config_var",
+                                                    lambda k: "other" if k == "SOABI" else real(k)))):
+        with monkeypatch.context() as m:
+            change(m)
+            assert not b.up_to_date()
+            b.build()
+            assert b.up_to_date() and len(tree.runs("cxx")) == 2 * (2 * n + 2)
+        assert not b.up_to_date()
+        b.build()
+        assert len(tree.runs("cxx")) == 2 * (2 * n + 3) and len(tree.runs("nvcc")) == 3
+
+
+def test_a_binding_of_another_torch_is_not_used(monkeypatch):
+    if not os.path.exists(os.path.join(ROOT, "selective_state_space_bwd_b200", "_ssm_torch.so")):
+        pytest.skip("needs the built binding")
+    import torch
+
+    from selective_state_space_bwd_b200 import build, ssm_scan
+    build.build()
+    monkeypatch.setattr(ssm_scan, "_torch_binding", None)
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.1")
+        with pytest.raises(RuntimeError, match="was built against"):
+            ssm_scan._native()
+    assert ssm_scan._native() is not None

@@ -522,8 +522,11 @@ int ssm_conv_step(const ssm_conv_serve* shape, const void* x, const float* w, co
  * x, delta_raw, z, y [rows, D], Bm, Cm [rows, N] io type; A_log [D, N], Dskip [D] fp32. */
 typedef struct ssm_scan_serve {
     int64_t rows, seqs, dim, dstate, slots; /* dim at most 2^20, N one of 4, 8, 16; else as above */
-    int64_t max_len; /* prompts: no sequence is longer (0 = rows); by it the call decides whether the
-                        lengths differ enough to start the longest first.  Single tokens: must be 0 */
+    int64_t max_len; /* prompts: no sequence is longer (0 = rows).  With rows and dim it picks the kernel, and
+                        so the rounding: one for a few long sequences, one for many; and whether the longest are
+                        started first.  Give the longest length where the host knows it: a call with 0 is taken for
+                        one long sequence, which costs a batch of many half as much time again.  Single tokens:
+                        must be 0 */
     int64_t ldx, lddelta, ldz, ldb, ldc, ldy;
     int32_t io;             /* ssm_dtype */
     int32_t discretization; /* ssm_discretization */

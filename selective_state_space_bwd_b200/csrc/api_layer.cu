@@ -81,7 +81,8 @@ int check_index(const int32_t* offsets, const int32_t* slot, bool prompts) {
 }
 
 // Sequences or rows that may name pool entries: each is compared with all before it by every CTA that
-// works on it (4096: half a gigabyte of cached loads in all for 4096 single tokens of 4096 channels).
+// works on it.  4096 single tokens of 4096 channels with 16 states take 64 tiles of channels a row, 2.1 GB of cached
+// loads: 475 us, against 358 without slots, which need no comparison.
 constexpr int64_t kMaxNamed = 4096;
 
 int check_rows(int64_t rows, int64_t seqs, int64_t slots, bool prompts) {

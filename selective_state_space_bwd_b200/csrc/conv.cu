@@ -1,8 +1,9 @@
 // Short causal convolution in front of the scan: forward, its recomputation from an 8-bit
 // checkpoint, its gradient, and the packed-prompt and single-token forms (include/ssm_scan.h).
 //
-// Every kernel is bound by memory traffic, with the instructions (SiLU, conversion, W products) and,
-// in the gradient, the fp32 pipes not far behind.  A thread owns V consecutive
+// The plain forward and the gradient run at 85 to 90 % of the copy bandwidth on large inputs.  The 8-bit forms in
+// bf16 (60 to 77 %; in fp32 80 to 85 %) issue an instruction in half of the cycles at 14 warps an SM, and wait for the
+// latency of the ones before it (SiLU, conversion, W products).  A thread owns V consecutive
 // channels and walks down a piece of the rows, the last W-1 inputs in registers, so that an element
 // is read once from DRAM (the W-1 rows before a piece a second time).  Each thread copies its
 // own rows into its own places of a ring in shared memory, kDepth - 1 groups of four rows ahead
@@ -222,7 +223,7 @@ template <typename E, int V, int W, bool SILU, bool SRC8, bool DST8>
 struct Fwd {
     using R = Rows<E, V, SRC8>;
     // Groups in the ring: one or two on their way.  Bytes in flight are not what the forward waits for: at
-    // 4 x 8192 x 4096 it takes 94 us with one group of 16-byte rows ahead, 103 with two to four.
+    // 4 x 8192 x 4096 it takes 92 us with one group of 16-byte rows ahead, 103 with two to four.
     static constexpr int kDepth = sizeof(typename R::Raw) == 16 ? 2 : 3;
     static constexpr int kBytes = kDepth * U * kThreads * (int)sizeof(typename R::Raw);
 };
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvArgs a) {
         const E* dy = static_cast<const E*>(a.dy) + (size_t)b * a.L * a.lddy + c;
         const unsigned lddyb = (unsigned)(a.lddy * sizeof(E)), lddxb = (unsigned)(a.lddx * sizeof(E));
         // Rows are issued in order, so their addresses are running sums (one addition a row instead of a
-        // wide product: 152 -> 145 us at 4 x 8192 x 4096, 168 -> 161 from 8 bits).
+        // wide product: 152 -> 146 us at 4 x 8192 x 4096, 173 -> 168 from 8 bits).
         uintptr_t gp = (uintptr_t)row_at(dy, t0, lddyb), xp = (uintptr_t)rows.at(t0);
         auto issue = [&](int t, int stage) {
             auto one = [&](int u, bool there) {
@@ -678,7 +679,9 @@ cudaError_t dispatch(int width, bool silu, int io_bf16, F f) {
 
 // Rows a piece of one batch entry: as many as give one wave of CTAs, at least 8 (the W-1 rows before a
 // piece are read twice) and at most 512 (the gradient adds a piece's rows one after another in fp32;
-// its sums over pieces are pairwise or short).  A multiple of four: a word of step exponents.
+// then a CTA its ry <= 64 pieces, and the reduction an eighth of the
+// CTAs' sums and eight more, so that a sum is a chain of 512 + 64 + parts / 8 + 8 additions at most: 900 at
+// 32768 rows x 4096 channels).  A multiple of four: a word of step exponents.
 // `extra` pieces of the wave are kept free (a packed batch has up to one partly empty piece a sequence).
 int rows_per_piece(int64_t batch, int64_t rows, const Tile& t, int64_t extra) {
     if (batch < 1) batch = 1;

@@ -72,7 +72,8 @@ __device__ __forceinline__ void st_vec(E* p, const float2 (&v)[V / 2]) {
 // sigmoid(v) from the exp2 and reciprocal units.  exp(-v) overflows to infinity below -88, where the
 // quotient is zero, as sigmoid is to fp32's normal numbers.  (One reciprocal for two quotients was
 // tried: it saves one special-function operation in four but needs six instructions more a pair to
-// keep infinities and NaN apart, and the kernels are bound by instructions, not by that unit.)
+// keep infinities and NaN apart, and that unit is at most 59 % busy in these kernels: they wait for the fixed
+// latency of dependent instructions.)
 __device__ __forceinline__ float rcp_mufu(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -550,7 +550,9 @@ cudaError_t prompt_launch(const ScanServeArgs& a, unsigned ctas, cudaStream_t st
 // The forms cross where the few form's throughput meets the time that the longest sequence takes in the many
 // form, that is at a fixed number of CTAs' worth of full-length work, rows * ndt / max_len.  Measured on a
 // B200 (bf16, gated; us many / few): N = 16 at 351 201 / 166, at 411 56 / 84, at 678 48 / 76; N = 8 at 245
-// 158 / 108, at 339 34 / 43; N = 4 at 192 41 / 34, at 429 16 / 34.
+// 158 / 108, at 339 34 / 43; N = 4 at 192 41 / 34, at 429 16 / 34.  Without the caller's max_len it is the rows, as
+// of one sequence, and the few form is taken below kManyFrom tiles: 24 prompts of 9989 rows on 4096 channels then
+// take 481 us instead of 326.
 template <int N> constexpr int64_t kManyFrom = N == 16 ? 363 : (N == 8 ? 300 : 250);
 
 template <typename E, int N, bool ZOH>

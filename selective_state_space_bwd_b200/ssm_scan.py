@@ -688,7 +688,8 @@ def ssm_scan_prompt(x, delta_raw, A_log, Bm, Cm, Dskip, offsets, slots, pool, ca
     """Scan of packed prompts from and to a pool of states [slots, D, N] fp32 (updated in place), y
     times SiLU(z) when z is given.  x, delta_raw, z [R,D], Bm, Cm [R,N] in one io type, rows may be
     strided; offsets, slots, carry as for ssm_conv_prompt; ``max_len`` bounds the sequences' length
-    (0: the rows; a longer one is left out).  ``ws`` (256 bytes, optional) receives the status word.
+    (0: the rows; a longer one is left out) and picks the kernel: give the longest length, or a batch of many
+    prompts runs in the kernel for one long sequence.  ``ws`` (256 bytes, optional) receives the status word.
     Returns y [R,D]."""
     if offsets is None:
         raise ValueError("offsets is needed")
